@@ -396,6 +396,106 @@ ciera_status ciera_encode_ex(const void* d_x, uint64_t n, uint32_t B, uint8_t* d
                              uint64_t* d_out_size, int e0_override, uint32_t plan_groups,
                              hipStream_t stream);
 
+/* Microscaled matrices: a rows x cols BF16 matrix held in 8 bits (mx8) or 4
+ * bits (mx4) per value, each 32 consecutive values of a row (a block) with one
+ * power-of-two scale.  Unlike the codecs above this is lossy; the products
+ * below compute with what the encoded matrices stand for.  They are the parts
+ * of a linear layer, or of the experts of a mixture-of-experts layer, whose
+ * weights are held in mx4 and whose activations are kept for the backward
+ * pass (checkpointed) in mx8:
+ *   y  = x W^T    mx4_matmul (x in BF16), mx4_matmul_mx8 (x in mx8)
+ *   dx = dy W     mx4_matmul_dx, the gradient of x
+ *   dW = dy^T x   mx8_wgrad, the gradient of W, x in mx8
+ *
+ * Encoded matrix, one buffer of mx*_encoded_size(rows, cols) bytes: with Kp =
+ * cols rounded up to a multiple of 128,
+ *   values  row by row; mx8: Kp bytes a row, e4m3 (sign, 4 exponent bits of
+ *           bias 7, 3 significand bits; 0x7F and 0xFF would be NaN); mx4:
+ *           Kp / 2 bytes a row, e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ *           negatives), value 2j in the low half of byte j, 2j + 1 in the high;
+ *   zeros up to a multiple of 128 bytes;
+ *   scales  Kp / 32 bytes a row, byte b (1..254) standing for 2^(b - 127) and
+ *           255 for NaN.
+ * Columns cols .. Kp - 1 are zeros.  Encoding takes for each block the
+ * smallest scale for which no value exceeds the largest the element type
+ * holds (448 or 6), at least 2^-126, and rounds value / scale to nearest,
+ * ties to even; a value is off by at most half a step of its type's grid
+ * times the scale.  A block holding an infinity or a NaN gets scale byte 255
+ * and zero values, and stands for 32 NaN.  A matrix made elsewhere in this
+ * layout (zeros in the padding included) can be used as well.
+ *
+ * Sizes: rows <= 2^31; cols, n, k <= 2^21; groups <= 4096; groups * n <= 2^31;
+ * row strides (ld*, in values) from the number of columns to 2^22.  BF16 and
+ * FP32 matrices need the alignment of their type only, and rows may start
+ * anywhere; encoded matrices and the workspace are 16-byte aligned.
+ *
+ * Groups: the products take `groups` weight matrices of n x k at once, encoded
+ * as one matrix of groups * n rows.  Rows d_offsets[g] .. d_offsets[g + 1] - 1
+ * of x, y, dy and dx belong to group g (none when the two are equal); rows
+ * before the first and behind the last group's are neither read nor written.
+ * d_offsets: groups + 1 int64 on the device, not decreasing, within 0..tokens;
+ * null (one group only) stands for {0, tokens}.  A pair that decreases or
+ * leaves 0..tokens holds no rows, and ciera_read_error(d_ws) then reports
+ * CIERA_ERR_ARG.
+ *
+ * Sums are held in FP32 and rounded once, to nearest, when the output is
+ * BF16, with one exception: mx4_matmul_mx8 with a BF16 output may take a block's
+ * part of a sum from the scaled matrix instructions, which cut products below
+ * 2^-13 of the block's largest, so a block's part is off by at most 2^-8 of
+ * its largest product.  The order of a sum depends on the sizes only, so equal
+ * calls give equal bits.  Calls are asynchronous and launch only kernels; errors and the
+ * workspace's use are as for every entry point here. */
+
+/* Bytes of an encoded matrix; 0 when rows or cols is out of range (or the
+ * matrix is empty). */
+uint64_t mx8_encoded_size(uint64_t rows, uint64_t cols);
+uint64_t mx4_encoded_size(uint64_t rows, uint64_t cols);
+/* Workspace bytes of the four products (one size serves all of them); 0 when
+ * a size is out of range. */
+uint64_t mx_workspace_size(uint64_t tokens, uint64_t n, uint64_t k, uint32_t groups);
+
+/* mx8_encode, mx4_encode:  d_x  in, rows x cols BF16, row stride ld;  d_q  out,
+ * q_bytes >= the encoded size (else CIERA_ERR_CAPACITY). */
+ciera_status mx8_encode(const void* d_x, uint64_t rows, uint64_t cols, uint64_t ld, void* d_q, uint64_t q_bytes,
+                        hipStream_t stream);
+ciera_status mx4_encode(const void* d_x, uint64_t rows, uint64_t cols, uint64_t ld, void* d_q, uint64_t q_bytes,
+                        hipStream_t stream);
+
+/* mx8_decode, mx4_decode: the values the encoded matrix stands for, as BF16
+ * (exact; a magnitude that rounding took to 2^128 becomes infinity, a NaN
+ * block NaN).  q_bytes below the encoded size is CIERA_ERR_FORMAT. */
+ciera_status mx8_decode(const void* d_q, uint64_t q_bytes, uint64_t rows, uint64_t cols, void* d_y, uint64_t ld,
+                        hipStream_t stream);
+ciera_status mx4_decode(const void* d_q, uint64_t q_bytes, uint64_t rows, uint64_t cols, void* d_y, uint64_t ld,
+                        hipStream_t stream);
+
+/* mx4_matmul, mx4_matmul_mx8: y = x W^T.
+ *   d_x   in   tokens x k BF16, row stride ldx (mx4_matmul), or
+ *   d_xq  in   tokens x k mx8 of xq_bytes (mx4_matmul_mx8)
+ *   d_w   in   groups * n x k mx4 of w_bytes
+ *   d_y   out  tokens x n, row stride ldy: BF16 (y_f32 = 0) or FP32 (1)
+ *   d_ws  tmp  ws_bytes >= mx_workspace_size(tokens, n, k, groups)
+ * An encoded matrix below its size is CIERA_ERR_FORMAT. */
+ciera_status mx4_matmul(const void* d_x, uint64_t ldx, const void* d_w, uint64_t w_bytes, void* d_y, uint64_t ldy,
+                        uint32_t y_f32, uint64_t tokens, uint64_t n, uint64_t k, uint32_t groups,
+                        const int64_t* d_offsets, void* d_ws, uint64_t ws_bytes, hipStream_t stream);
+ciera_status mx4_matmul_mx8(const void* d_xq, uint64_t xq_bytes, const void* d_w, uint64_t w_bytes, void* d_y,
+                            uint64_t ldy, uint32_t y_f32, uint64_t tokens, uint64_t n, uint64_t k, uint32_t groups,
+                            const int64_t* d_offsets, void* d_ws, uint64_t ws_bytes, hipStream_t stream);
+
+/* mx4_matmul_dx: dx = dy W, dy tokens x n BF16, dx tokens x k BF16 or FP32. */
+ciera_status mx4_matmul_dx(const void* d_dy, uint64_t lddy, const void* d_w, uint64_t w_bytes, void* d_dx,
+                           uint64_t lddx, uint32_t dx_f32, uint64_t tokens, uint64_t n, uint64_t k, uint32_t groups,
+                           const int64_t* d_offsets, void* d_ws, uint64_t ws_bytes, hipStream_t stream);
+
+/* mx8_wgrad: dW_g = dy_g^T x_g, dy tokens x n BF16, x tokens x k mx8.  d_dw
+ * holds groups matrices of n x k, contiguous, BF16 or FP32; accumulate = 1
+ * adds the product to what is there (one rounding of the sum), 0 writes it,
+ * zeros for a group without rows. */
+ciera_status mx8_wgrad(const void* d_dy, uint64_t lddy, const void* d_xq, uint64_t xq_bytes, void* d_dw,
+                       uint32_t dw_f32, uint32_t accumulate, uint64_t tokens, uint64_t n, uint64_t k, uint32_t groups,
+                       const int64_t* d_offsets, void* d_ws, uint64_t ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

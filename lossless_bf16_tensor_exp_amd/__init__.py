@@ -31,6 +31,7 @@ Same names as the C ABI::
     ciera_time_kernels(pairs)             (profiling: per-kernel start/stop events)
     ciera_set_wait_limit(polls)           (test hook: bound of the waits between workgroups)
     ciera_encode_noalloc(x, B, prev_exp, out, out_size, stream=None)   (no workspace: allocates nothing)
+    mx8_* / mx4_*                         (8- and 4-bit matrices and their products: ``mx.py``)
 
 ``x``/``y`` are CUDA(HIP) tensors of dtype bfloat16, int16 or uint16 holding
 the BF16 patterns; ``out``/``inp``/``ws``/``prev_exp`` are uint8 tensors and
@@ -52,6 +53,8 @@ __all__ = [
     "decode_batch_workspace_size", "zip3_decode_batch", "ciera_decode_batch", "DECODE_BATCH_MAX",
     "zip3_encode_spec", "ciera_encode_spec",
     "CHUNK",
+    "mx8_encoded_size", "mx4_encoded_size", "mx_workspace_size", "mx8_encode", "mx8_decode", "mx4_encode", "mx4_decode",
+    "mx4_matmul", "mx4_matmul_mx8", "mx4_matmul_dx", "mx8_wgrad",
 ]
 
 CHUNK = 65536
@@ -476,3 +479,18 @@ def ciera_set_wait_limit(polls: int) -> int:
     """Test hook: polls after which the next calls' waits on other workgroups
     give up (0 restores the default).  Returns the previous bound."""
     return int(load_library().ciera_set_wait_limit(polls))
+
+
+_MX = ("mx8_encoded_size", "mx4_encoded_size", "mx_workspace_size", "mx8_encode", "mx8_decode", "mx4_encode",
+       "mx4_decode", "mx4_matmul", "mx4_matmul_mx8", "mx4_matmul_dx", "mx8_wgrad")
+
+
+def __getattr__(name):
+    """The microscaled matrices' calls, bound at first use: ``mx.py`` needs
+    torch, which importing this package does not load."""
+    if name in _MX:
+        from . import mx
+        for f in _MX:
+            globals()[f] = getattr(mx, f)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -11,7 +11,7 @@ import subprocess
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SRC = os.path.join(HERE, "csrc", "ciera.hip")
+SRC = os.path.join(HERE, "csrc", "libciera.hip")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libciera.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
