@@ -225,6 +225,7 @@ struct MxArgs {
   Ctrl* ctrl;
   uint32_t* status;
   uint32_t tokens, n, k, kp, groups;
+  uint32_t parts;  // wgrad: the contraction in this many parts, each with an output of its own
   uint32_t out_f32, accumulate;
 };
 
@@ -258,39 +259,70 @@ __device__ __forceinline__ void mx_report(const MxArgs& p) {
   }
 }
 
-// The group and rows of token tile `tile` of `1 << lbm` rows, tiles numbered
-// group by group.  Every wave finds it for itself: 64 groups a step, their
-// tile counts summed by a lane scan.
-__device__ __forceinline__ bool mx_find_tile(const MxArgs& p, uint32_t tile, uint32_t lbm, uint32_t& g, uint32_t& row0,
-                                             uint32_t& row1) {
-  if (!p.offsets) {
-    g = 0u;
-    row0 = tile << lbm;
-    row1 = p.tokens;
-    return row0 < row1;
-  }
+// Where this workgroup's tile is among the real ones.  Token tiles of 1 << lbm
+// rows are numbered group by group; every wave counts them for itself, 64
+// groups a step by a lane scan.  `ntiles` column tiles belong to each.  The
+// grid is as large as any offsets can need; the workgroups past the real tiles
+// end.  Workgroups go to the eight XCDs in turn, so tiles are dealt out in
+// eight runs: an XCD's L2 then holds the weights of its own few groups and the
+// rows they share.
+struct MxTile {
+  uint32_t g, row0, row1, col;
+};
+__device__ __forceinline__ uint32_t mx_xcd_run(uint32_t block, uint32_t total) {
+  const uint32_t xcd = block & 7u, per = total >> 3, rem = total & 7u;
+  return xcd * per + min(xcd, rem) + (block >> 3);
+}
+__device__ __forceinline__ uint32_t mx_scan(uint32_t v) {
   const uint32_t lane = threadIdx.x & 63u;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t up = uint32_t(__shfl_up(int(v), d));
+    if (lane >= uint32_t(d)) v += up;
+  }
+  return v;
+}
+__device__ __forceinline__ uint32_t mx_first(uint32_t v) { return uint32_t(__builtin_amdgcn_readfirstlane(int(v))); }
+__device__ __forceinline__ bool mx_find_tile(const MxArgs& p, uint32_t lbm, uint32_t ntiles, MxTile& t) {
+  const uint32_t lane = threadIdx.x & 63u, up = (1u << lbm) - 1u;
+  if (!p.offsets) {
+    const uint32_t at = mx_xcd_run(blockIdx.x, gridDim.x);
+    t.g = 0u;
+    t.row0 = (at / ntiles) << lbm;
+    t.row1 = p.tokens;
+    t.col = at % ntiles;
+    return true;
+  }
+  uint32_t r0 = 0u, r1 = 0u, sum = 0u, total = 0u;
+  for (uint32_t c = 0; c < p.groups; c += 64u) {
+    r0 = r1 = 0u;
+    if (c + lane < p.groups) mx_rows(p, c + lane, r0, r1);
+    sum = mx_scan((r1 - r0 + up) >> lbm);
+    total += uint32_t(__builtin_amdgcn_readlane(int(sum), 63));
+  }
+  if (blockIdx.x >= total * ntiles) return false;
+  const uint32_t at = mx_xcd_run(blockIdx.x, total * ntiles);
+  const uint32_t tile = at / ntiles;
+  t.col = at - tile * ntiles;
   uint32_t before = 0u;
   for (uint32_t c = 0; c < p.groups; c += 64u) {
-    uint32_t r0 = 0u, r1 = 0u;
-    if (c + lane < p.groups) mx_rows(p, c + lane, r0, r1);
-    const uint32_t mine = (r1 - r0 + (1u << lbm) - 1u) >> lbm;
-    uint32_t sum = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const uint32_t up = uint32_t(__shfl_up(int(sum), d));
-      if (lane >= uint32_t(d)) sum += up;
+    if (p.groups > 64u) {
+      r0 = r1 = 0u;
+      if (c + lane < p.groups) mx_rows(p, c + lane, r0, r1);
+      sum = mx_scan((r1 - r0 + up) >> lbm);
     }
     const uint64_t past = __ballot(before + sum > tile);
     if (past) {
       const int l = __ffsll((unsigned long long)past) - 1;
-      const uint32_t skip = tile - (before + uint32_t(__shfl(int(sum - mine), l)));
-      g = uint32_t(__builtin_amdgcn_readfirstlane(int(c) + l));
-      row0 = uint32_t(__builtin_amdgcn_readfirstlane(__shfl(int(r0), l) + int(skip << lbm)));
-      row1 = uint32_t(__builtin_amdgcn_readfirstlane(__shfl(int(r1), l)));
+      const uint32_t a = uint32_t(__builtin_amdgcn_readlane(int(r0), l));
+      const uint32_t b = uint32_t(__builtin_amdgcn_readlane(int(r1), l));
+      const uint32_t end = before + uint32_t(__builtin_amdgcn_readlane(int(sum), l));
+      t.g = c + uint32_t(l);
+      t.row0 = a + ((tile - (end - ((b - a + up) >> lbm))) << lbm);
+      t.row1 = b;
       return true;
     }
-    before += uint32_t(__shfl(int(sum), 63));
+    before += uint32_t(__builtin_amdgcn_readlane(int(sum), 63));
   }
   return false;
 }
@@ -308,221 +340,381 @@ __device__ __forceinline__ void mx_store(const MxArgs& p, uint64_t at, float v) 
   }
 }
 
+// Stores of 4 FP32 or 4 / 8 BF16 values at any address of the type.
+typedef float v4fa4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x2a2 __attribute__((ext_vector_type(2), aligned(2)));
+
+__device__ __forceinline__ uint32_t mx_bf16x2(float lo, float hi) {
+  return uint32_t(mx_bf16(lo)) | uint32_t(mx_bf16(hi)) << 16;
+}
+
+__device__ __forceinline__ void mx_store4(const MxArgs& p, uint64_t at, v4f x) {
+  if (p.out_f32) {
+    v4fa4* o = reinterpret_cast<v4fa4*>(static_cast<float*>(p.out) + at);
+    if (p.accumulate) x += v4f(*o);
+    *o = x;
+  } else {
+    u32x2a2* o = reinterpret_cast<u32x2a2*>(static_cast<uint16_t*>(p.out) + at);
+    if (p.accumulate) {
+      const u32x2v w = *o;
+      x[0] += mx_f32(uint16_t(w[0]));
+      x[1] += mx_f32(uint16_t(w[0] >> 16));
+      x[2] += mx_f32(uint16_t(w[1]));
+      x[3] += mx_f32(uint16_t(w[1] >> 16));
+    }
+    *o = u32x2v{mx_bf16x2(x[0], x[1]), mx_bf16x2(x[2], x[3])};
+  }
+}
+
+// One 32 x 32 fragment of sums to the output.  The matrix instructions take
+// the output's columns as their rows, so a lane holds one output row, lane %
+// 32, and its register r column 8 (r / 4) + 4 (lane / 32) + r % 4: four
+// neighbours at a time.  In BF16 the lane halves first exchange every other
+// four, which leaves each with eight neighbours, 16 bytes.
+__device__ __forceinline__ void mx_store_frag(const MxArgs& p, bool row_ok, uint64_t row_at, uint32_t col0,
+                                              uint32_t cols, const v16f& v) {
+  const uint32_t half = (threadIdx.x >> 5) & 1u;
+  const bool whole = col0 + 32u <= cols;
+  if (whole && !p.out_f32 && !p.accumulate) {
+    uint16_t* o = static_cast<uint16_t*>(p.out) + row_at + col0 + 8u * half;
+#pragma unroll
+    for (int q = 0; q < 4; q += 2) {
+      u32x4v w;
+#pragma unroll
+      for (int i = 0; i < 2; i++) {
+        const auto x = __builtin_amdgcn_permlane32_swap(mx_bf16x2(v[4 * q + 2 * i], v[4 * q + 2 * i + 1]),
+                                                        mx_bf16x2(v[4 * q + 4 + 2 * i], v[4 * q + 5 + 2 * i]), false, false);
+        w[i] = x[0];
+        w[2 + i] = x[1];
+      }
+      if (row_ok) *reinterpret_cast<u32x4a2*>(o + 8 * q) = w;
+    }
+    return;
+  }
+  if (!row_ok) return;
+#pragma unroll
+  for (int q = 0; q < 4; q++) {
+    const uint32_t col = col0 + 8u * uint32_t(q) + 4u * half;
+    if (col + 4u <= cols) {
+      mx_store4(p, row_at + col, v4f{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]});
+    } else {
+#pragma unroll
+      for (uint32_t i = 0; i < 3u; i++)
+        if (col + i < cols) mx_store(p, row_at + col + i, v[4 * q + int(i)]);
+    }
+  }
+}
+
 enum MxOp { kMxMatmul = 0, kMxDx = 1, kMxWgrad = 2, kMxMatmul8 = 3 };
 
-constexpr uint32_t kMxBN = 128u;  // output columns of a tile
-constexpr uint32_t kMxBC = 64u;   // contraction values staged per step (BF16 products)
 
-// Byte offsets in the staged tiles.  "Rows": row r of 64 contraction values,
-// 128 bytes, its 16-byte chunks exclusive-ored with r / 2, so that the 32
-// rows a fragment read touches fall on all banks.  "Cols": contraction row c
-// of `cols` values, its 64-byte pieces exclusive-ored with c, so that the
-// four rows a transposing read gathers fall on different banks.
-__device__ __forceinline__ uint32_t mx_rows_at(uint32_t r, uint32_t chunk) {
-  return r * 128u + ((chunk ^ ((r >> 1) & 7u)) << 4);
+// Loads from global memory straight into LDS: lane i's 16 (or 4) bytes at
+// base + off land at lds + 16 i (4 i).  No register holds them, so they stay
+// in flight over whole steps; mx_fence counts them.
+__device__ __forceinline__ void mx_dma16(uint32_t off, const void* base, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :: "v"(off), "s"(base), "s"(lds) : "memory");
 }
-__device__ __forceinline__ uint32_t mx_cols_at(uint32_t c, uint32_t byte, uint32_t cols) {
-  return c * cols * 2u + (byte ^ ((c & 3u) << 6));
+__device__ __forceinline__ void mx_dma4(uint32_t off, const void* base, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
+               :: "v"(off), "s"(base), "s"(lds) : "memory");
+}
+// All but this wave's last kLeft loads have landed, its LDS reads and writes
+// are done, and so are every other wave's.
+template <int kLeft>
+__device__ __forceinline__ void mx_fence() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"(kLeft) : "memory");
+}
+__device__ __forceinline__ uint32_t mx_lds(const void* at) {
+  return uint32_t(uintptr_t((__attribute__((address_space(3))) const void*)at));
 }
 
-__device__ __forceinline__ v8bf mx_read_rows(const uint8_t* tile, uint32_t r, uint32_t chunk) {
-  return *reinterpret_cast<const v8bf*>(tile + mx_rows_at(r, chunk));
+// Staged tiles.  A row of R bytes is kept as 16-byte chunks; chunk c of row r
+// sits at c ^ mx_turn<R>(r), so that lanes which read (or write) one chunk of
+// 16 consecutive rows touch all 64 banks once.  The loads above apply it by
+// choosing which chunk a lane fetches.
+template <uint32_t kRow>
+__device__ __forceinline__ uint32_t mx_turn(uint32_t r) {
+  return kRow >= 256u ? (r & 15u) : (r / (256u / kRow)) & (kRow / 16u - 1u);
 }
-// Eight contraction values c0 .. c0 + 7 of one column per lane: two reads
-// that each transpose 4 rows x 16 columns within 16 lanes.
-__device__ __forceinline__ v8bf mx_read_cols(const uint8_t* tile, uint32_t c0, uint32_t col0, uint32_t cols) {
+template <uint32_t kRow>
+__device__ __forceinline__ uint32_t mx_at(uint32_t r, uint32_t chunk) {
+  return r * kRow + ((chunk ^ mx_turn<kRow>(r)) << 4);
+}
+// A tile to be read transposed: contraction row c of kRow bytes.  The 64-byte
+// piece is exclusive-ored with c, so the four rows a transposing read gathers
+// differ in bank, and the chunk within it with c / 4, for the writers.
+__device__ __forceinline__ uint32_t mx_turn_cols(uint32_t c) { return ((c & 3u) << 2) ^ ((c >> 2) & 3u); }
+
+// Eight contraction values c0 .. c0 + 7 (c0 a multiple of 8) of one column per
+// lane: two reads that each transpose 4 rows x 16 columns within 16 lanes.
+// at0, at1: this lane's addresses for c0 = 0 and its two reads.
+__device__ __forceinline__ v8bf mx_read_cols(const uint8_t* at0, const uint8_t* at1) {
   typedef __attribute__((address_space(3))) v4s lds_v4s;
-  const uint32_t l = threadIdx.x & 15u;
-  const uint32_t byte = (col0 + (l & 3u) * 4u) * 2u;
-  const uint32_t c = c0 + (l >> 2);
-  const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(tile + mx_cols_at(c, byte, cols)));
-  const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(tile + mx_cols_at(c + 4u, byte, cols)));
+  const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)at0);
+  const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)at1);
   const v4s both[2] = {lo, hi};
   return __builtin_bit_cast(v8bf, both);
 }
 
-// The products on BF16 matrix instructions: tiles of kBM x 128 outputs, four
-// waves, 64 contraction values per step.  The mx operand becomes BF16 on its
-// way into LDS; a wave keeps its 32 x 32 sums in registers.
-//   matmul  M tokens, N weight rows, contraction k:  both operands run along
-//           the contraction in memory; x in BF16 or mx8
-//   dx      M tokens, N k, contraction n:  W's rows are contraction rows, read
-//           back transposed
-//   wgrad   M n, N k, contraction tokens of the group:  both transposed
-template <int kOp, uint32_t kBM>
-__global__ __launch_bounds__(kMxThreads, 2) void k_mx_gemm(MxArgs p) {
-  __shared__ __attribute__((aligned(16))) uint8_t s_a[kBM * 128u];
-  __shared__ __attribute__((aligned(16))) uint8_t s_b[kMxBN * 128u];
+// The products on BF16 matrix instructions: tiles of kBM x kBN outputs, kWM x
+// kWN waves, 64 contraction values a step, a ring of kStages steps in LDS
+// filled by loads that need no registers, one barrier a step.  A wave keeps
+// its 32 x 32 sums in registers.
+//   matmul  M tokens, N weight rows, contraction k: both operands run along
+//           the contraction.  W stays in 4 bits in LDS: a lane reads a whole
+//           block of 32 of its row (16 bytes) and makes BF16 of it next to the
+//           matrix instructions, a quarter of the LDS traffic of a BF16 tile.
+//           Lane half h so holds values 32 h .. 32 h + 31 of the step, eight
+//           per instruction; x is read in the same order.  x in mx8 likewise.
+//   dx      M tokens, N k, contraction n: W's rows are contraction rows; its
+//           scales differ along them, so it becomes BF16 on the way to a
+//           second LDS tile (one step ahead) that is read back transposed.
+//   wgrad   M n, N k, contraction the group's tokens: the same for x, and dy
+//           is read back transposed too.
+template <int kOp, uint32_t kBM, uint32_t kBN, uint32_t kBC, uint32_t kWM, uint32_t kWN, uint32_t kStages, uint32_t kPerCu>
+__global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_gemm(MxArgs p) {
   constexpr bool kRowsB = kOp == kMxMatmul || kOp == kMxMatmul8;  // B runs along the contraction
-  constexpr uint32_t kAChunks = kBM * (kOp == kMxMatmul8 ? 4u : 8u) / kMxThreads;  // 16-byte loads of A per thread
-  constexpr uint32_t kBChunks = kOp == kMxWgrad ? 2u : 1u;
-  constexpr uint32_t kFM = kBM / 64u;  // 32-row fragments of a wave
-  constexpr uint32_t kFN = 2u;
-  const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
+  constexpr uint32_t kW = kWM * kWN;
+  constexpr uint32_t kABytes = kBM * kBC * (kOp == kMxMatmul8 ? 1u : 2u);       // of a step's A
+  constexpr uint32_t kARow = kOp == kMxWgrad ? kBM * 2u : kABytes / kBM;
+  constexpr uint32_t kAPer = kARow / 16u;
+  constexpr uint32_t kBBits = kOp == kMxWgrad ? 8u : 4u;
+  constexpr uint32_t kRawBytes = kBN * kBC * kBBits / 8u;                       // of a step's mx operand B
+  constexpr uint32_t kRawRow = kRawBytes / (kRowsB ? kBN : kBC);
+  constexpr uint32_t kRawPer = kRawRow / 16u;
+  constexpr uint32_t kScaleWords = kRowsB ? 0u : (kBC * (kBN / 128u) + 63u) / 64u * 64u;  // four scale bytes each, whole waves
+  constexpr uint32_t kStage = kABytes + kRawBytes + 4u * kScaleWords;
+  // matmul: 16 scale bytes of every row at a time, eight steps' worth, twice
+  constexpr uint32_t kScaleRows = kRowsB ? kBN + (kOp == kMxMatmul8 ? kBM : 0u) : 0u;
+  constexpr uint32_t kTile = kRowsB ? 0u : kBN * kBC * 2u;                      // B in BF16
+  constexpr uint32_t kFM = kBM / kWM / 32u, kFN = kBN / kWN / 32u;              // 32 x 32 sums of a wave
+  constexpr uint32_t kSub = kBC / 16u;                                          // matrix instructions along a step
+  constexpr uint32_t kALoads = kABytes / 1024u, kRawLoads = kRawBytes / 1024u;  // of all waves; fewer than waves: some repeat
+  constexpr uint32_t kDmaA = kALoads < kW ? 1u : kALoads / kW;                  // per wave and step
+  constexpr uint32_t kDmaRaw = kRawLoads < kW ? 1u : kRawLoads / kW;
+  constexpr uint32_t kDma = kDmaA + kDmaRaw;
+  static_assert(kALoads * 1024u == kABytes && (kALoads < kW ? kW % kALoads == 0u : kALoads % kW == 0u), "whole loads");
+  static_assert(kRawLoads * 1024u == kRawBytes && (kRawLoads < kW ? kW % kRawLoads == 0u : kRawLoads % kW == 0u), "whole loads");
+  static_assert(kScaleWords <= 64u * kW && kScaleRows % 64u == 0u, "whole waves");
+  static_assert(!kRowsB || kBC == 64u, "a lane half takes a block of 32");
+  __shared__ __attribute__((aligned(256))) uint8_t lds[kStages * kStage + 2u * kTile + 32u * kScaleRows];
+  const uint32_t tid = threadIdx.x, lane = tid & 63u, half = lane >> 5;
+  const uint32_t wave = mx_first(tid >> 6);
   if (blockIdx.x == 0u) mx_report(p);
 
   // where the tile is: its group, its output rows m0 .. m1 - 1 and columns
   uint32_t g, m0, m1, n0, c1;
   const uint32_t cols = kRowsB ? p.n : p.k;
-  const uint32_t ntiles = (cols + kMxBN - 1u) / kMxBN;
-  uint32_t r0 = 0u;  // first contraction row (wgrad)
+  const uint32_t ntiles = (cols + kBN - 1u) / kBN;
+  uint32_t r0 = 0u, part = 0u;  // first contraction row, and which part of them (wgrad)
   if constexpr (kOp == kMxWgrad) {
     const uint32_t mtiles = (p.n + kBM - 1u) / kBM;
-    g = blockIdx.x / (mtiles * ntiles);
-    const uint32_t t = blockIdx.x - g * (mtiles * ntiles);
-    m0 = (t / ntiles) * kBM;
-    n0 = (t % ntiles) * kMxBN;
+    const uint32_t at = mx_xcd_run(blockIdx.x, gridDim.x);
+    const uint32_t gp = at / (mtiles * ntiles);
+    const uint32_t t = at - gp * (mtiles * ntiles);
+    part = gp / p.groups;
+    g = gp - part * p.groups;
+    m0 = (t % mtiles) * kBM;
+    n0 = (t / mtiles) * kBN;
     m1 = p.n;
-    uint32_t r1;
-    mx_rows(p, g, r0, r1);
-    c1 = r1 - r0;
+    uint32_t a, b;
+    mx_rows(p, g, a, b);
+    const uint32_t each = (b - a + p.parts - 1u) / p.parts;
+    const uint32_t from = min(part * each, b - a);
+    r0 = mx_first(a + from);
+    c1 = mx_first(min(each, b - a - from));
   } else {
-    const uint32_t t = blockIdx.x / ntiles;
-    n0 = (blockIdx.x - t * ntiles) * kMxBN;
-    constexpr uint32_t kLog = kBM == 256u ? 8u : 6u;
-    if (!mx_find_tile(p, t, kLog, g, m0, m1)) return;
+    MxTile t;
+    if (!mx_find_tile(p, kBM == 256u ? 8u : kBM == 128u ? 7u : kBM == 64u ? 6u : 5u, ntiles, t)) return;
+    g = t.g;
+    m0 = t.row0;
+    m1 = t.row1;
+    n0 = t.col * kBN;
     c1 = kRowsB ? p.k : p.n;
   }
-  const uint32_t steps = (c1 + kMxBC - 1u) / kMxBC;
+  const uint32_t steps = (c1 + kBC - 1u) / kBC;
+  const uint32_t lds0 = mx_lds(lds);
 
-  // A: byte offsets of this thread's chunks from the tile's first row
-  const uint8_t* a_base;
-  const uint8_t* as_base = nullptr;  // the scales of an mx8 A
-  uint32_t a_off[kAChunks];
+  // A's loads.  Lanes fetch 16-byte chunks at these offsets from the tile's
+  // first row (wgrad: from the step's first); rows and columns past the
+  // operand's end are fetched from its last (their sums are not stored).
+  // Where rows are not 16-byte aligned, and where the contraction ends inside
+  // a step, fill_a goes through registers instead.
+  const bool wide = kOp == kMxMatmul8 || ((reinterpret_cast<uintptr_t>(p.a) & 15u) == 0u && (p.lda & 7u) == 0u &&
+                                          (kOp != kMxWgrad || (p.n & 7u) == 0u));
+  const uint8_t* a_next;  // of the step to be loaded next
+  uint64_t a_stride = kARow;
+  uint32_t a_off[kDmaA];
   if constexpr (kOp == kMxWgrad) {
-    a_base = reinterpret_cast<const uint8_t*>(p.a + uint64_t(r0) * p.lda + m0);
-  } else if constexpr (kOp == kMxMatmul8) {
-    a_base = p.xq + uint64_t(m0) * p.kp;
-    as_base = p.xs + uint64_t(m0) * (p.kp / 32u);
+    a_next = reinterpret_cast<const uint8_t*>(p.a + uint64_t(r0) * p.lda + m0);
+    a_stride = p.lda * (2u * kBC);
 #pragma unroll
-    for (uint32_t i = 0; i < kAChunks; i++)
-      a_off[i] = min(i * 64u + (tid >> 2), m1 - 1u - m0) * p.kp + (tid & 3u) * 16u;
+    for (uint32_t i = 0; i < kDmaA; i++) {
+      const uint32_t pos = (i * kW + wave) % kALoads * 64u + lane, c = pos / kAPer;
+      const uint32_t col = ((pos % kAPer) ^ mx_turn_cols(c)) * 8u;
+      a_off[i] = c * uint32_t(p.lda) * 2u + (min(m0 + col, p.n - 8u) - m0) * 2u;
+    }
   } else {
-    a_base = reinterpret_cast<const uint8_t*>(p.a + uint64_t(m0) * p.lda);
+    const uint64_t pitch = kOp == kMxMatmul8 ? p.kp : p.lda * 2u;
+    a_next = (kOp == kMxMatmul8 ? p.xq : reinterpret_cast<const uint8_t*>(p.a)) + uint64_t(m0) * pitch;
 #pragma unroll
-    for (uint32_t i = 0; i < kAChunks; i++) {
-      const uint32_t r = min(i * 32u + (tid >> 3), m1 - 1u - m0);
-      a_off[i] = r * uint32_t(p.lda) * 2u + (tid & 7u) * 16u;
+    for (uint32_t i = 0; i < kDmaA; i++) {
+      const uint32_t pos = (i * kW + wave) % kALoads * 64u + lane, r = pos / kAPer;
+      a_off[i] = min(r, m1 - 1u - m0) * uint32_t(pitch) + ((pos % kAPer) ^ mx_turn<kARow>(r)) * 16u;
     }
   }
-  u32x4v va[kAChunks];
-  uint32_t sa[kAChunks];
-  v4i vb[kBChunks];
-  uint32_t sb[kBChunks];
-
-  const auto load_a = [&](uint32_t step) {
-    const uint32_t c0 = step * kMxBC;
-    if constexpr (kOp == kMxWgrad) {
-      // contraction row c0 + i * 8 + tid / 32 (kBM = 256), 8 columns
-      constexpr uint32_t kPerRow = kBM / 8u;
-      const uint32_t col = (tid % kPerRow) * 8u;
-      const uint8_t* base = a_base + uint64_t(c0) * p.lda * 2u;
-      const bool edge = m0 + kBM > p.n;
-#pragma unroll
-      for (uint32_t i = 0; i < kAChunks; i++) {
-        const uint32_t r = (i * kMxThreads + tid) / kPerRow;
-        const uint32_t rc = min(r, c1 - 1u - c0);
-        const uint8_t* src = base + rc * uint32_t(p.lda) * 2u;
-        if (!edge) {
-          va[i] = *reinterpret_cast<const u32x4a2*>(src + col * 2u);
-        } else {  // columns past n are not read
-          const uint32_t have = m0 + col < p.n ? p.n - m0 - col : 0u;
-          va[i] = mx_part8(reinterpret_cast<const uint16_t*>(src) + (have ? col : 0u), have);
-        }
-        if (c0 + kMxBC > c1 && r != rc) va[i] = u32x4v{0u, 0u, 0u, 0u};
+  const auto fill_a = [&](uint32_t step, uint8_t* to) {
+    const uint32_t c0 = step * kBC;
+#pragma unroll 1
+    for (uint32_t i = 0; i < kDmaA; i++) {
+      const uint32_t pos = (i * kW + wave) % kALoads * 64u + lane, r = pos / kAPer;
+      uint32_t have;
+      uint64_t at;
+      if constexpr (kOp == kMxWgrad) {
+        const uint32_t col = m0 + ((pos % kAPer) ^ mx_turn_cols(r)) * 8u;
+        have = c0 + r < c1 && col < p.n ? p.n - col : 0u;
+        at = (uint64_t(r0) + c0 + r) * p.lda + col;
+      } else {
+        const uint32_t c = c0 + ((pos % kAPer) ^ mx_turn<kARow>(r)) * 8u;
+        have = c < c1 ? c1 - c : 0u;
+        at = (uint64_t(m0) + min(r, m1 - 1u - m0)) * p.lda + c;
       }
-    } else if constexpr (kOp == kMxMatmul8) {
-#pragma unroll
-      for (uint32_t i = 0; i < kAChunks; i++) {
-        va[i] = *reinterpret_cast<const u32x4v*>(a_base + a_off[i] + c0);
-        sa[i] = as_base[(a_off[i] + c0) / 32u];
-      }
+      const uint16_t* src = p.a + (have ? at : 0u);
+      *reinterpret_cast<u32x4v*>(to + pos * 16u) =
+          have >= 8u ? u32x4v(*reinterpret_cast<const u32x4a2*>(src)) : mx_part8(src, have);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the count of loads in flight starts anew
+  };
+  const auto load_a = [&](uint32_t step, uint32_t slot) {
+    const uint32_t at = slot * kStage;
+    if (kOp != kMxMatmul8 && (!wide || (step + 1u) * kBC > c1)) {
+      fill_a(step, lds + at);
     } else {
-      const uint8_t* base = a_base + c0 * 2u;
-      if (c0 + kMxBC <= c1) {
 #pragma unroll
-        for (uint32_t i = 0; i < kAChunks; i++) va[i] = *reinterpret_cast<const u32x4a2*>(base + a_off[i]);
-      } else {  // the contraction ends in this step: zeros behind it
-        const uint32_t c = c0 + (tid & 7u) * 8u;
+      for (uint32_t i = 0; i < kDmaA; i++) mx_dma16(a_off[i], a_next, lds0 + at + (i * kW + wave) % kALoads * 1024u);
+    }
+    a_next += a_stride;
+  };
+
+  // the mx operand's loads
+  const uint8_t* b_next;
+  const uint8_t* bs_next;
+  uint32_t b_off[kDmaRaw], b_row[kDmaRaw], bs_off = 0u, bs_row = 0u;
+  const uint32_t b_pitch = p.kp * kBBits / 8u, s_pitch = p.kp / 32u;
+  {
+    const uint64_t row = kOp == kMxWgrad ? uint64_t(r0) : uint64_t(g) * p.n + (kRowsB ? n0 : 0u);
+    b_next = (kOp == kMxWgrad ? p.xq : p.wq) + row * b_pitch;
+    bs_next = (kOp == kMxWgrad ? p.xs : p.ws) + row * s_pitch;
 #pragma unroll
-        for (uint32_t i = 0; i < kAChunks; i++) {
-          va[i] = mx_part8(reinterpret_cast<const uint16_t*>(base + a_off[i]), c < c1 ? c1 - c : 0u);
-        }
-      }
+    for (uint32_t i = 0; i < kDmaRaw; i++) {
+      const uint32_t pos = (i * kW + wave) % kRawLoads * 64u + lane, r = pos / kRawPer;
+      b_row[i] = r;
+      if constexpr (kRowsB) b_off[i] = min(r, p.n - 1u - n0) * b_pitch + (pos % kRawPer) * 16u;
+      else b_off[i] = min(n0 * kBBits / 8u + ((pos % kRawPer) ^ mx_turn<kRawRow>(r)) * 16u, b_pitch - 16u);
+    }
+    if constexpr (!kRowsB) {
+      constexpr uint32_t kWords = kBN / 128u;
+      bs_row = tid / kWords;
+      bs_off = min(n0 / 32u + (tid % kWords) * 4u, s_pitch - 4u);
+    }
+  }
+  // matmul: bytes from the scales of a row of W (r < kBN) or x to the end of
+  // all; a row's 16 may reach past that and are then the section's last 16,
+  // `late` bytes early.
+  const auto scales_left = [&](uint32_t r) {
+    const uint64_t rows = r < kBN ? uint64_t(p.groups - g) * p.n - n0 - min(r, p.n - 1u - n0)
+                                  : uint64_t(p.tokens) - m0 - min(r - kBN, m1 - 1u - m0);
+    return int(min(rows * s_pitch, uint64_t(1u << 30)));
+  };
+  const auto late = [](int left, uint32_t chunk) { return uint32_t(max(int(chunk * 16u + 16u) - left, 0)); };
+  constexpr uint32_t kScaleLoads = kRowsB ? (kScaleRows + 64u * kW - 1u) / (64u * kW) : 1u;
+  uint32_t sc_off[kScaleLoads];
+  int sc_left[kScaleLoads];
+  const uint8_t* const as_first = kOp == kMxMatmul8 ? p.xs + uint64_t(m0) * s_pitch - 16 : nullptr;
+  const uint8_t* const bs_first = bs_next - 16;  // the offsets are 16 up, so that early ones stay positive
+  if constexpr (kRowsB) {
+#pragma unroll
+    for (uint32_t i = 0; i < kScaleLoads; i++) {
+      const uint32_t r = i * 64u * kW + tid;
+      sc_off[i] = 16u + (r < kBN ? min(r, p.n - 1u - n0) : min(r - kBN, m1 - 1u - m0)) * s_pitch;
+      sc_left[i] = scales_left(r);
+    }
+  }
+  const auto scales_at = [](uint32_t chunk) { return kStages * kStage + 16u * kScaleRows * (chunk & 1u); };
+  const auto load_scales = [&](uint32_t chunk) {
+#pragma unroll
+    for (uint32_t i = 0; i < kScaleLoads; i++) {
+      const uint32_t first = i * 64u * kW + wave * 64u;
+      if (first < kScaleRows)
+        mx_dma16(sc_off[i] + chunk * 16u - late(sc_left[i], chunk), first < kBN ? bs_first : as_first,
+                 lds0 + scales_at(chunk) + first * 16u);
     }
   };
-  const auto load_b = [&](uint32_t step) {
-    const uint32_t c0 = step * kMxBC;
-    if constexpr (kRowsB) {  // weight row n0 + tid / 2, one block of 32
-      const uint64_t row = uint64_t(g) * p.n + min(n0 + (tid >> 1), p.n - 1u);
-      const uint32_t at = c0 + (tid & 1u) * 32u;
-      vb[0] = *reinterpret_cast<const v4i*>(p.wq + row * (p.kp / 2u) + at / 2u);
-      sb[0] = p.ws[row * (p.kp / 32u) + at / 32u];
-    } else if constexpr (kOp == kMxDx) {  // contraction row c0 + tid / 4, one block of 32
-      const uint32_t c = c0 + (tid >> 2);
-      const uint64_t row = uint64_t(g) * p.n + min(c, c1 - 1u);
-      const uint32_t at = n0 + (tid & 3u) * 32u;
-      vb[0] = *reinterpret_cast<const v4i*>(p.wq + row * (p.kp / 2u) + at / 2u);
-      sb[0] = p.ws[row * (p.kp / 32u) + at / 32u];
-      if (c >= c1) {
-        vb[0] = v4i{0, 0, 0, 0};
-        sb[0] = 127u;
-      }
-    } else {  // contraction row c0 + i * 32 + tid / 8, 16 values of a block
+  const auto load_b = [&](uint32_t step, uint32_t slot) {
+    const uint32_t at = lds0 + slot * kStage + kABytes;
+    if constexpr (kRowsB) {
 #pragma unroll
-      for (uint32_t i = 0; i < kBChunks; i++) {
-        const uint32_t c = c0 + i * 32u + (tid >> 3);
-        const uint64_t row = uint64_t(r0) + min(c, c1 - 1u);
-        const uint32_t at = n0 + (tid & 7u) * 16u;
-        vb[i] = *reinterpret_cast<const v4i*>(p.xq + row * p.kp + at);
-        sb[i] = p.xs[row * (p.kp / 32u) + at / 32u];
-        if (c >= c1) {
-          vb[i] = v4i{0, 0, 0, 0};
-          sb[i] = 127u;
-        }
-      }
-    }
-  };
-  const auto stage = [&]() {
+      for (uint32_t i = 0; i < kDmaRaw; i++) mx_dma16(b_off[i], b_next, at + (i * kW + wave) % kRawLoads * 1024u);
+      b_next += kRawRow;
+    } else {
+      // rows behind the contraction's end are fetched from its last; past the
+      // last step the load repeats it, so that every batch counts the same
+      const uint32_t last = min(c1 - 1u - step * kBC, kBC - 1u);
 #pragma unroll
-    for (uint32_t i = 0; i < kAChunks; i++) {
-      if constexpr (kOp == kMxMatmul8) {
-        const float s = mx_scale(sa[i]);
-#pragma unroll
-        for (uint32_t h = 0; h < 2u; h++)
-          *reinterpret_cast<u32x4v*>(s_a + mx_rows_at(i * 64u + (tid >> 2), (tid & 3u) * 2u + h)) =
-              mx_unit8(va[i][2u * h], va[i][2u * h + 1u], s);
-        continue;
-      }
-      uint32_t at;
-      if constexpr (kOp == kMxWgrad) {
-        constexpr uint32_t kPerRow = kBM / 8u;
-        at = mx_cols_at((i * kMxThreads + tid) / kPerRow, (tid % kPerRow) * 16u, kBM);
-      } else {
-        at = mx_rows_at(i * 32u + (tid >> 3), tid & 7u);
-      }
-      *reinterpret_cast<u32x4v*>(s_a + at) = va[i];
-    }
-#pragma unroll
-    for (uint32_t i = 0; i < kBChunks; i++) {
-      const float s = mx_scale(sb[i]);
-      if constexpr (kOp == kMxWgrad) {
-#pragma unroll
-        for (uint32_t h = 0; h < 2u; h++)
-          *reinterpret_cast<u32x4v*>(s_b + mx_cols_at(i * 32u + (tid >> 3), (tid & 7u) * 32u + h * 16u, kMxBN)) =
-              mx_unit8(uint32_t(vb[i][2u * h]), uint32_t(vb[i][2u * h + 1u]), s);
-      } else {
-#pragma unroll
-        for (uint32_t h = 0; h < 4u; h++) {
-          const uint32_t at = kRowsB ? mx_rows_at(tid >> 1, (tid & 1u) * 4u + h)
-                                               : mx_cols_at(tid >> 2, (tid & 3u) * 64u + h * 16u, kMxBN);
-          *reinterpret_cast<u32x4v*>(s_b + at) = mx_unit4(uint32_t(vb[i][h]), s);
-        }
+      for (uint32_t i = 0; i < kDmaRaw; i++)
+        mx_dma16(min(b_row[i], last) * b_pitch + b_off[i], b_next, at + (i * kW + wave) % kRawLoads * 1024u);
+      if (wave * 64u < kScaleWords)
+        mx_dma4(min(bs_row, last) * s_pitch + bs_off, bs_next, at + kRawBytes + wave * 256u);
+      if (step + 1u < steps) {
+        b_next += uint64_t(kBC) * b_pitch;
+        bs_next += uint64_t(kBC) * s_pitch;
       }
     }
   };
 
-  const uint32_t wm = (wave >> 1) * (kBM / 2u), wn = (wave & 1u) * 64u;
+  // The mx operand of a step as BF16.  A thread takes 8-byte units (8 values
+  // of mx8, 16 of mx4) of one contraction row, lanes next to each other in
+  // neighbouring rows.
+  constexpr uint32_t kUnits = kTile ? kRawBytes / (512u * kW) : 1u;
+  constexpr uint32_t kPer = 8u / kBBits;  // 16-byte pieces of BF16 in a unit
+  const uint32_t raw_row = tid % kBC;
+  u32x2v raw[kUnits];
+  float raw_s[kUnits];
+  const auto raw_read = [&](uint32_t step, uint32_t slot) {
+    const uint8_t* q = lds + slot * kStage + kABytes;
+#pragma unroll
+    for (uint32_t i = 0; i < kUnits; i++) {
+      const uint32_t unit = tid / kBC + i * (64u * kW / kBC);
+      raw[i] = *reinterpret_cast<const u32x2v*>(q + mx_at<kRawRow>(raw_row, unit >> 1) + (unit & 1u) * 8u);
+      raw_s[i] = mx_scale(q[kRawBytes + raw_row * (kBN / 32u) + unit * kPer / 4u]);
+    }
+    if ((step + 1u) * kBC > c1) {  // zeros behind the contraction's end
+#pragma unroll
+      for (uint32_t i = 0; i < kUnits; i++)
+        if (step * kBC + raw_row >= c1) {
+          raw[i] = u32x2v{0u, 0u};
+          raw_s[i] = 1.0f;
+        }
+    }
+  };
+  const auto raw_write = [&](uint32_t part, uint8_t* tile) {  // part of kSub
+    constexpr uint32_t kPieces = kUnits * kPer;
+#pragma unroll
+    for (uint32_t piece = 0; piece < kPieces; piece++) {
+      if (piece * kSub / kPieces != part) continue;
+      const uint32_t i = piece / kPer, h = piece % kPer;
+      const uint32_t unit = tid / kBC + i * (64u * kW / kBC);
+      const uint32_t at = raw_row * (kBN * 2u) + (((unit * kPer + h) ^ mx_turn_cols(raw_row)) << 4);
+      *reinterpret_cast<u32x4v*>(tile + at) =
+          kOp == kMxWgrad ? mx_unit8(raw[i][0], raw[i][1], raw_s[i]) : mx_unit4(raw[i][h], raw_s[i]);
+    }
+  };
+
+  // A wave's row fragments lie kWM apart, so that where the group's rows end
+  // inside the tile every wave has as few left (matmul, dx).
+  const uint32_t wm = (wave / kWN) * 32u, wn = (wave % kWN) * (kBN / kWN);
+  constexpr uint32_t kMStep = kWM * 32u;
   v16f acc[kFM][kFN];
 #pragma unroll
   for (uint32_t i = 0; i < kFM; i++)
@@ -531,59 +723,141 @@ __global__ __launch_bounds__(kMxThreads, 2) void k_mx_gemm(MxArgs p) {
 #pragma unroll
       for (int r = 0; r < 16; r++) acc[i][j][r] = 0.0f;
 
+  // Batch b of loads: A of step b and the mx operand of step b (matmul) or
+  // b + 1, whose BF16 tile is made during step b.  kStages - 1 batches are in
+  // flight while a step computes.
+  const auto next_slot = [](uint32_t s) { return s + 1u == kStages ? 0u : s + 1u; };
+  const auto batch = [&](uint32_t b, uint32_t slot) {
+    if constexpr (kRowsB)
+      if (b % 8u == 0u) load_scales(b / 8u);
+    load_a(b, slot);
+    if constexpr (kRowsB) load_b(b, slot);
+    else load_b(min(b + 1u, steps - 1u), next_slot(slot));
+  };
+  // All but the last kBatches batches have landed.  Every wave counts its own
+  // loads: those that fetch scale words have one more in each batch (in a
+  // matmul's every eighth, where waiting for it too costs nothing).
+  const auto fence = [&](auto batches) {
+    constexpr int kBatches = decltype(batches)::value;
+    if (!kRowsB && wave * 64u < kScaleWords) mx_fence<kBatches * int(kDma + 1u)>();
+    else mx_fence<kBatches * int(kDma)>();
+  };
   if (steps) {
-    load_a(0u);
-    load_b(0u);
-  }
-  for (uint32_t step = 0; step < steps; step++) {
-    if (step) __syncthreads();
-    stage();
-    __syncthreads();
-    if (step + 1u < steps) {
-      load_a(step + 1u);
-      load_b(step + 1u);
+    if constexpr (!kRowsB) load_b(0u, 0u);
+#pragma unroll
+    for (uint32_t b = 0; b + 1u < kStages; b++)
+      if (b < steps) batch(b, b);
+    if constexpr (!kRowsB) {
+      if (steps + 1u >= kStages) fence(std::integral_constant<int, int(kStages) - 1>());
+      else mx_fence<0>();
+      raw_read(0u, 0u);
+#pragma unroll
+      for (uint32_t q = 0; q < kSub; q++) raw_write(q, lds + kStages * kStage);
     }
+  }
+  int left_b[kFN], left_a[kFM];
+  if constexpr (kRowsB) {
 #pragma unroll
-    for (uint32_t s = 0; s < kMxBC / 16u; s++) {
-      v8bf fa[kFM], fb[kFN];
+    for (uint32_t j = 0; j < kFN; j++) left_b[j] = scales_left(wn + j * 32u + (lane & 31u));
 #pragma unroll
-      for (uint32_t i = 0; i < kFM; i++) {
-        if constexpr (kOp == kMxWgrad)
-          fa[i] = mx_read_cols(s_a, s * 16u + (lane >> 5) * 8u, wm + i * 32u + ((lane >> 4) & 1u) * 16u, kBM);
-        else
-          fa[i] = mx_read_rows(s_a, wm + i * 32u + (lane & 31u), s * 2u + (lane >> 5));
-      }
+    for (uint32_t i = 0; i < kFM; i++) left_a[i] = kOp == kMxMatmul8 ? scales_left(kBN + wm + i * kMStep + (lane & 31u)) : 0;
+  }
+  uint32_t slot = 0u, load_slot = kStages - 1u;
+  for (uint32_t step = 0; step < steps; step++) {
+    if (step + kStages - 1u <= steps) fence(std::integral_constant<int, int(kStages) - 2>());
+    else mx_fence<0>();
+    if (step + kStages - 1u < steps) batch(step + kStages - 1u, load_slot);
+    load_slot = slot;
+    const uint8_t* sa = lds + slot * kStage;
+    if constexpr (kRowsB) {
+      const uint8_t* sb = sa + kABytes;
+      // this step's scale byte of a row lies at ss + 16 row, or later
+      const uint32_t chunk = step / 8u;
+      const uint8_t* ss = lds + scales_at(chunk) + (step % 8u) * 2u + half;
+      v4i rb[kFN];
+      float bs[kFN];
 #pragma unroll
       for (uint32_t j = 0; j < kFN; j++) {
-        if constexpr (kRowsB)
-          fb[j] = mx_read_rows(s_b, wn + j * 32u + (lane & 31u), s * 2u + (lane >> 5));
-        else
-          fb[j] = mx_read_cols(s_b, s * 16u + (lane >> 5) * 8u, wn + j * 32u + ((lane >> 4) & 1u) * 16u, kMxBN);
+        const uint32_t r = wn + j * 32u + (lane & 31u);
+        rb[j] = *reinterpret_cast<const v4i*>(sb + r * 32u + half * 16u);
+        bs[j] = mx_scale(ss[r * 16u + late(left_b[j], chunk)]);
       }
+      u32x4v ra[kFM][2];
+      float as[kFM];
+      if constexpr (kOp == kMxMatmul8) {
 #pragma unroll
-      for (uint32_t i = 0; i < kFM; i++)
-#pragma unroll
-        for (uint32_t j = 0; j < kFN; j++)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
-    }
-  }
-
-  // a fragment's register r holds row 8 (r / 4) + 4 (lane / 32) + r % 4 of
-  // column lane % 32
-#pragma unroll
-  for (uint32_t i = 0; i < kFM; i++)
-#pragma unroll
-    for (uint32_t j = 0; j < kFN; j++) {
-      const uint32_t col = n0 + wn + j * 32u + (lane & 31u);
-#pragma unroll
-      for (uint32_t r = 0; r < 16u; r++) {
-        const uint32_t row = m0 + wm + i * 32u + 8u * (r / 4u) + 4u * (lane >> 5) + (r & 3u);
-        if (row < m1 && col < cols) {
-          if constexpr (kOp == kMxWgrad) mx_store(p, (uint64_t(g) * p.n + row) * p.k + col, acc[i][j][r]);
-          else mx_store(p, uint64_t(row) * p.ldo + col, acc[i][j][r]);
+        for (uint32_t i = 0; i < kFM; i++) {
+          const uint32_t r = wm + i * kMStep + (lane & 31u);
+          ra[i][0] = *reinterpret_cast<const u32x4v*>(sa + mx_at<64u>(r, half * 2u));
+          ra[i][1] = *reinterpret_cast<const u32x4v*>(sa + mx_at<64u>(r, half * 2u + 1u));
+          as[i] = mx_scale(ss[(kBN + r) * 16u + late(left_a[i], chunk)]);
         }
       }
+#pragma unroll
+      for (uint32_t s = 0; s < 4u; s++) {
+        v8bf fa[kFM], fb[kFN];
+#pragma unroll
+        for (uint32_t i = 0; i < kFM; i++) {
+          if constexpr (kOp == kMxMatmul8)
+            fa[i] = __builtin_bit_cast(v8bf, mx_unit8(ra[i][s / 2u][(s % 2u) * 2u], ra[i][s / 2u][(s % 2u) * 2u + 1u], as[i]));
+          else
+            fa[i] = *reinterpret_cast<const v8bf*>(sa + mx_at<128u>(wm + i * kMStep + (lane & 31u), half * 4u + s));
+        }
+#pragma unroll
+        for (uint32_t j = 0; j < kFN; j++) fb[j] = __builtin_bit_cast(v8bf, mx_unit4(uint32_t(rb[j][s]), bs[j]));
+#pragma unroll
+        for (uint32_t i = 0; i < kFM; i++)
+#pragma unroll
+          for (uint32_t j = 0; j < kFN; j++)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+      }
+    } else {
+      const uint8_t* tile = lds + kStages * kStage + (step & 1u) * kTile;
+      uint8_t* next = lds + kStages * kStage + ((step + 1u) & 1u) * kTile;
+      if (step + 1u < steps) raw_read(step + 1u, next_slot(slot));
+      v8bf fa[2][kFM], fb[2][kFN];
+      const auto frags = [&](uint32_t s, v8bf* to_a, v8bf* to_b) {
+        // this lane's contraction row of a transposing read, and its turn
+        const uint32_t c = s * 16u + half * 8u + ((lane >> 2) & 3u);
+        const uint32_t t0 = mx_turn_cols(c) << 4, t1 = mx_turn_cols(c + 4u) << 4;
+        const uint32_t piece = ((lane >> 4) & 1u) * 32u + (lane & 3u) * 8u;
+#pragma unroll
+        for (uint32_t i = 0; i < kFM; i++) {
+          if constexpr (kOp == kMxWgrad) {
+            const uint32_t byte = (wm + i * kMStep) * 2u + piece;
+            to_a[i] = mx_read_cols(sa + c * kARow + (byte ^ t0), sa + (c + 4u) * kARow + (byte ^ t1));
+          } else {
+            to_a[i] = *reinterpret_cast<const v8bf*>(sa + mx_at<kARow>(wm + i * kMStep + (lane & 31u), s * 2u + half));
+          }
+        }
+#pragma unroll
+        for (uint32_t j = 0; j < kFN; j++) {
+          const uint32_t byte = (wn + j * 32u) * 2u + piece;
+          to_b[j] = mx_read_cols(tile + c * (kBN * 2u) + (byte ^ t0), tile + (c + 4u) * (kBN * 2u) + (byte ^ t1));
+        }
+      };
+      frags(0u, fa[0], fb[0]);
+#pragma unroll
+      for (uint32_t s = 0; s < kSub; s++) {
+        if (s + 1u < kSub) frags(s + 1u, fa[(s + 1u) & 1u], fb[(s + 1u) & 1u]);
+#pragma unroll
+        for (uint32_t i = 0; i < kFM; i++)
+#pragma unroll
+          for (uint32_t j = 0; j < kFN; j++)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[s & 1u][j], fa[s & 1u][i], acc[i][j], 0, 0, 0);
+        if (step + 1u < steps) raw_write(s, next);
+      }
     }
+    slot = next_slot(slot);
+  }
+
+#pragma unroll
+  for (uint32_t i = 0; i < kFM; i++) {
+    const uint32_t row = m0 + wm + i * kMStep + (lane & 31u);
+    const uint64_t at = kOp == kMxWgrad ? ((uint64_t(part) * p.groups + g) * p.n + row) * p.k : uint64_t(row) * p.ldo;
+#pragma unroll
+    for (uint32_t j = 0; j < kFN; j++) mx_store_frag(p, row < m1, at, n0 + wn + j * 32u, cols, acc[i][j]);
+  }
 }
 
 // matmul of an mx8 operand with a BF16 result: the scaled matrix instructions
@@ -595,52 +869,82 @@ __global__ __launch_bounds__(kMxThreads, 2) void k_mx_gemm(MxArgs p) {
 // largest product.  On activations with a few loud channels the result moved
 // by 1/7 of a BF16 rounding at the most; where the caller asks for FP32 it
 // would show, and k_mx_gemm computes that.  128 contraction values (four
-// blocks) per step; the padded pitch leaves no partial step.
-template <uint32_t kBM>
-__global__ __launch_bounds__(kMxThreads, 2) void k_mx_gemm8(MxArgs p) {
-  __shared__ __attribute__((aligned(16))) uint8_t s_a[kBM * 128u];
-  __shared__ __attribute__((aligned(16))) uint8_t s_b[kMxBN * 64u];
-  __shared__ uint32_t s_sa[kBM], s_sb[kMxBN];  // a row's four scale bytes
-  constexpr uint32_t kAChunks = kBM * 8u / kMxThreads;
-  constexpr uint32_t kFM = kBM / 64u;
-  constexpr uint32_t kFN = 2u;
-  const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
+// blocks) a step, the ring and the tile as in k_mx_gemm; the padded pitch
+// leaves no partial step.
+template <uint32_t kBM, uint32_t kBN, uint32_t kWM, uint32_t kWN, uint32_t kStages, uint32_t kPerCu>
+__global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_gemm8(MxArgs p) {
+  constexpr uint32_t kW = kWM * kWN;
+  constexpr uint32_t kABytes = kBM * 128u, kRawBytes = kBN * 64u;
+  constexpr uint32_t kStage = kABytes + kRawBytes;
+  // 16 scale bytes of every row (W's, then x's) at a time, four steps' worth, twice
+  constexpr uint32_t kScaleRows = (kBN + kBM + 63u) / 64u * 64u;
+  constexpr uint32_t kFM = kBM / kWM / 32u, kFN = kBN / kWN / 32u;
+  constexpr uint32_t kDmaA = kABytes / (1024u * kW), kDmaB = kRawBytes / (1024u * kW);
+  constexpr uint32_t kDma = kDmaA + kDmaB;
+  static_assert(kDmaA * 1024u * kW == kABytes && kDmaB * 1024u * kW == kRawBytes, "whole loads for every wave");
+  static_assert(kBN % 64u == 0u, "whole waves");
+  __shared__ __attribute__((aligned(256))) uint8_t lds[kStages * kStage + 32u * kScaleRows];
+  const uint32_t tid = threadIdx.x, lane = tid & 63u, half = lane >> 5;
+  const uint32_t wave = uint32_t(__builtin_amdgcn_readfirstlane(int(tid >> 6)));
   if (blockIdx.x == 0u) mx_report(p);
-  const uint32_t ntiles = (p.n + kMxBN - 1u) / kMxBN;
-  const uint32_t t = blockIdx.x / ntiles;
-  const uint32_t n0 = (blockIdx.x - t * ntiles) * kMxBN;
-  uint32_t g, m0, m1;
-  constexpr uint32_t kLog = kBM == 256u ? 8u : 6u;
-  if (!mx_find_tile(p, t, kLog, g, m0, m1)) return;
+  MxTile t;
+  if (!mx_find_tile(p, kBM == 256u ? 8u : kBM == 128u ? 7u : kBM == 64u ? 6u : 5u, (p.n + kBN - 1u) / kBN, t)) return;
+  const uint32_t m0 = t.row0, m1 = t.row1, n0 = t.col * kBN;
+  const uint32_t lds0 = mx_lds(lds);
 
   const uint8_t* a_base = p.xq + uint64_t(m0) * p.kp;
   const uint8_t* as_base = p.xs + uint64_t(m0) * (p.kp / 32u);
-  const uint8_t* b_base = p.wq + (uint64_t(g) * p.n + n0) * (p.kp / 2u);
-  const uint8_t* bs_base = p.ws + (uint64_t(g) * p.n + n0) * (p.kp / 32u);
-  uint32_t a_off[kAChunks], b_off[2];
+  const uint8_t* b_base = p.wq + (uint64_t(t.g) * p.n + n0) * (p.kp / 2u);
+  const uint8_t* bs_base = p.ws + (uint64_t(t.g) * p.n + n0) * (p.kp / 32u);
+  uint32_t a_off[kDmaA], b_off[kDmaB];
 #pragma unroll
-  for (uint32_t i = 0; i < kAChunks; i++)
-    a_off[i] = min(i * 32u + (tid >> 3), m1 - 1u - m0) * p.kp + (tid & 7u) * 16u;
+  for (uint32_t i = 0; i < kDmaA; i++) {
+    const uint32_t pos = (i * kW + wave) * 64u + lane, r = pos >> 3;
+    a_off[i] = min(r, m1 - 1u - m0) * p.kp + ((pos & 7u) ^ mx_turn<128u>(r)) * 16u;
+  }
 #pragma unroll
-  for (uint32_t i = 0; i < 2u; i++)
-    b_off[i] = min(i * 64u + (tid >> 2), p.n - 1u - n0) * (p.kp / 2u) + (tid & 3u) * 16u;
-  const uint32_t as_off = min(tid, m1 - 1u - m0) * (p.kp / 32u);
-  const uint32_t bs_off = min(tid & (kMxBN - 1u), p.n - 1u - n0) * (p.kp / 32u);
-  u32x4v va[kAChunks], vb[2];
-  uint32_t vsa, vsb;
-  const auto load = [&](uint32_t step) {
-#pragma unroll
-    for (uint32_t i = 0; i < kAChunks; i++)
-      va[i] = *reinterpret_cast<const u32x4v*>(a_base + a_off[i] + step * 128u);
-#pragma unroll
-    for (uint32_t i = 0; i < 2u; i++) vb[i] = *reinterpret_cast<const u32x4v*>(b_base + b_off[i] + step * 64u);
-    vsa = *reinterpret_cast<const uint32_t*>(as_base + as_off + step * 4u);
-    vsb = *reinterpret_cast<const uint32_t*>(bs_base + bs_off + step * 4u);
+  for (uint32_t i = 0; i < kDmaB; i++) {
+    const uint32_t pos = (i * kW + wave) * 64u + lane, r = pos >> 2;
+    b_off[i] = min(r, p.n - 1u - n0) * (p.kp / 2u) + ((pos & 3u) ^ mx_turn<64u>(r)) * 16u;
+  }
+  // scales: as in k_mx_gemm
+  const uint32_t s_pitch = p.kp / 32u;
+  const auto scales_left = [&](uint32_t r) {
+    const uint64_t rows = r < kBN ? uint64_t(p.groups - t.g) * p.n - n0 - min(r, p.n - 1u - n0)
+                                  : uint64_t(p.tokens) - m0 - min(r - kBN, m1 - 1u - m0);
+    return int(min(rows * s_pitch, uint64_t(1u << 30)));
   };
-  // 64-byte rows of B: chunks exclusive-ored with row / 4
-  const auto b_at = [](uint32_t r, uint32_t chunk) { return r * 64u + ((chunk ^ ((r >> 2) & 3u)) << 4); };
+  const auto late = [](int left, uint32_t chunk) { return uint32_t(max(int(chunk * 16u + 16u) - left, 0)); };
+  constexpr uint32_t kScaleLoads = (kScaleRows + 64u * kW - 1u) / (64u * kW);
+  uint32_t sc_off[kScaleLoads];
+  int sc_left[kScaleLoads];
+#pragma unroll
+  for (uint32_t i = 0; i < kScaleLoads; i++) {
+    const uint32_t r = i * 64u * kW + tid;
+    sc_off[i] = 16u + (r < kBN ? min(r, p.n - 1u - n0) : min(r - kBN, m1 - 1u - m0)) * s_pitch;
+    sc_left[i] = scales_left(r);
+  }
+  const auto scales_at = [](uint32_t chunk) { return kStages * kStage + 16u * kScaleRows * (chunk & 1u); };
+  const auto batch = [&](uint32_t step, uint32_t slot) {
+    const uint32_t at = lds0 + slot * kStage;
+    if (step % 4u == 0u) {
+      const uint32_t chunk = step / 4u;
+#pragma unroll
+      for (uint32_t i = 0; i < kScaleLoads; i++) {
+        const uint32_t first = i * 64u * kW + wave * 64u;
+        if (first < kScaleRows)
+          mx_dma16(sc_off[i] + chunk * 16u - late(sc_left[i], chunk), (first < kBN ? bs_base : as_base) - 16,
+                   lds0 + scales_at(chunk) + first * 16u);
+      }
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < kDmaA; i++) mx_dma16(a_off[i], a_base + step * 128u, at + (i * kW + wave) * 1024u);
+#pragma unroll
+    for (uint32_t i = 0; i < kDmaB; i++) mx_dma16(b_off[i], b_base + step * 64u, at + kABytes + (i * kW + wave) * 1024u);
+  };
 
-  const uint32_t wm = (wave >> 1) * (kBM / 2u), wn = (wave & 1u) * 64u;
+  const uint32_t wm = (wave / kWN) * 32u, wn = (wave % kWN) * (kBN / kWN);
+  constexpr uint32_t kMStep = kWM * 32u;
   v16f acc[kFM][kFN];
 #pragma unroll
   for (uint32_t i = 0; i < kFM; i++)
@@ -649,42 +953,53 @@ __global__ __launch_bounds__(kMxThreads, 2) void k_mx_gemm8(MxArgs p) {
 #pragma unroll
       for (int r = 0; r < 16; r++) acc[i][j][r] = 0.0f;
 
-  const uint32_t steps = p.kp / 128u, half = lane >> 5;
-  load(0u);
+  const uint32_t steps = p.kp / 128u;
+#pragma unroll
+  for (uint32_t b = 0; b + 1u < kStages; b++)
+    if (b < steps) batch(b, b);
+  int left_a[kFM], left_b[kFN];
+#pragma unroll
+  for (uint32_t i = 0; i < kFM; i++) left_a[i] = scales_left(kBN + wm + i * kMStep + (lane & 31u));
+#pragma unroll
+  for (uint32_t j = 0; j < kFN; j++) left_b[j] = scales_left(wn + j * 32u + (lane & 31u));
+  uint32_t slot = 0u, load_slot = kStages - 1u;
   for (uint32_t step = 0; step < steps; step++) {
-    if (step) __syncthreads();
-#pragma unroll
-    for (uint32_t i = 0; i < kAChunks; i++)
-      *reinterpret_cast<u32x4v*>(s_a + mx_rows_at(i * 32u + (tid >> 3), tid & 7u)) = va[i];
-#pragma unroll
-    for (uint32_t i = 0; i < 2u; i++)
-      *reinterpret_cast<u32x4v*>(s_b + b_at(i * 64u + (tid >> 2), tid & 3u)) = vb[i];
-    if (tid < kBM) s_sa[tid] = vsa;
-    if (tid < kMxBN) s_sb[tid] = vsb;
-    __syncthreads();
-    if (step + 1u < steps) load(step + 1u);
+    if (step + kStages - 1u <= steps) mx_fence<int((kStages - 2u) * kDma)>();
+    else mx_fence<0>();
+    if (step + kStages - 1u < steps) batch(step + kStages - 1u, load_slot);
+    load_slot = slot;
+    const uint8_t* s_a = lds + slot * kStage;
+    const uint8_t* s_b = s_a + kABytes;
+    const uint32_t chunk = step / 4u;
+    const uint8_t* s_s = lds + scales_at(chunk) + (step % 4u) * 4u + half;
     // Lane half h holds block 2 s + h of B's row, and of A's row the 16
     // values at 16 h and at 32 + 16 h of the 64; its scale byte is block
-    // 2 s + h's.  The byte the instruction picks is the same for all lanes,
-    // so the word is shifted by h first.
+    // 2 s + h's.  Both bytes of a step sit in one word, the instruction picks
+    // byte 0 or 2 of it.
     uint32_t sa[kFM], sb[kFN];
 #pragma unroll
-    for (uint32_t i = 0; i < kFM; i++) sa[i] = s_sa[wm + i * 32u + (lane & 31u)] >> (8u * half);
+    for (uint32_t i = 0; i < kFM; i++) {
+      const uint8_t* at = s_s + (kBN + wm + i * kMStep + (lane & 31u)) * 16u + late(left_a[i], chunk);
+      sa[i] = at[0] | uint32_t(at[2]) << 16;
+    }
 #pragma unroll
-    for (uint32_t j = 0; j < kFN; j++) sb[j] = s_sb[wn + j * 32u + (lane & 31u)] >> (8u * half);
+    for (uint32_t j = 0; j < kFN; j++) {
+      const uint8_t* at = s_s + (wn + j * 32u + (lane & 31u)) * 16u + late(left_b[j], chunk);
+      sb[j] = at[0] | uint32_t(at[2]) << 16;
+    }
 #pragma unroll
     for (uint32_t s = 0; s < 2u; s++) {
       v8i fa[kFM], fb[kFN];
 #pragma unroll
       for (uint32_t i = 0; i < kFM; i++) {
-        const uint32_t r = wm + i * 32u + (lane & 31u);
-        const v4i lo = *reinterpret_cast<const v4i*>(s_a + mx_rows_at(r, s * 4u + half));
-        const v4i hi = *reinterpret_cast<const v4i*>(s_a + mx_rows_at(r, s * 4u + 2u + half));
+        const uint32_t r = wm + i * kMStep + (lane & 31u);
+        const v4i lo = *reinterpret_cast<const v4i*>(s_a + mx_at<128u>(r, s * 4u + half));
+        const v4i hi = *reinterpret_cast<const v4i*>(s_a + mx_at<128u>(r, s * 4u + 2u + half));
         fa[i] = v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
       }
 #pragma unroll
       for (uint32_t j = 0; j < kFN; j++) {
-        const v4i q = *reinterpret_cast<const v4i*>(s_b + b_at(wn + j * 32u + (lane & 31u), s * 2u + half));
+        const v4i q = *reinterpret_cast<const v4i*>(s_b + mx_at<64u>(wn + j * 32u + (lane & 31u), s * 2u + half));
         fb[j] = v8i{q[0], q[1], q[2], q[3], 0, 0, 0, 0};
       }
 #pragma unroll
@@ -692,25 +1007,22 @@ __global__ __launch_bounds__(kMxThreads, 2) void k_mx_gemm8(MxArgs p) {
 #pragma unroll
         for (uint32_t j = 0; j < kFN; j++) {
           if (s == 0u)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[i], fb[j], acc[i][j], 0, 4, 0, int(sa[i]), 0,
-                                                                        int(sb[j]));
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[j], fa[i], acc[i][j], 4, 0, 0, int(sb[j]), 0,
+                                                                        int(sa[i]));
           else
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[i], fb[j], acc[i][j], 0, 4, 2, int(sa[i]), 2,
-                                                                        int(sb[j]));
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[j], fa[i], acc[i][j], 4, 0, 2, int(sb[j]), 2,
+                                                                        int(sa[i]));
         }
     }
+    slot = slot + 1u == kStages ? 0u : slot + 1u;
   }
 #pragma unroll
-  for (uint32_t i = 0; i < kFM; i++)
+  for (uint32_t i = 0; i < kFM; i++) {
+    const uint32_t row = m0 + wm + i * kMStep + (lane & 31u);
 #pragma unroll
-    for (uint32_t j = 0; j < kFN; j++) {
-      const uint32_t col = n0 + wn + j * 32u + (lane & 31u);
-#pragma unroll
-      for (uint32_t r = 0; r < 16u; r++) {
-        const uint32_t row = m0 + wm + i * 32u + 8u * (r / 4u) + 4u * half + (r & 3u);
-        if (row < m1 && col < p.n) mx_store(p, uint64_t(row) * p.ldo + col, acc[i][j][r]);
-      }
-    }
+    for (uint32_t j = 0; j < kFN; j++)
+      mx_store_frag(p, row < m1, uint64_t(row) * p.ldo, n0 + wn + j * 32u, p.n, acc[i][j]);
+  }
 }
 
 // matmul for few tokens a group: bound by reading the weights once.  A
@@ -785,6 +1097,22 @@ __global__ __launch_bounds__(kMxFewWaves * 64u) void k_mx_few(MxArgs p) {
 
 __global__ void k_mx_status(MxArgs p) { mx_report(p); }
 
+// wgrad's parts added in order; four values a thread.
+__global__ __launch_bounds__(kMxThreads) void k_mx_join(MxArgs p, const float* __restrict__ sums, uint64_t count) {
+  const uint64_t at = (uint64_t(blockIdx.x) * kMxThreads + threadIdx.x) * 4u;
+  if (at + 4u <= count && count % 4u == 0u) {
+    v4f v = *reinterpret_cast<const v4f*>(sums + at);
+    for (uint32_t i = 1; i < p.parts; i++) v += *reinterpret_cast<const v4f*>(sums + i * count + at);
+    mx_store4(p, at, v);
+  } else {
+    for (uint64_t j = at; j < at + 4u && j < count; j++) {
+      float v = sums[j];
+      for (uint32_t i = 1; i < p.parts; i++) v += sums[i * count + j];
+      mx_store(p, j, v);
+    }
+  }
+}
+
 ciera_status mx_matrix(const void* d_m, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t align) {
   if (rows > kMxMaxRows || cols > kMxMaxCols || ld < cols || ld > kMxMaxLd) return CIERA_ERR_ARG;
   if (rows && cols && (!d_m || (reinterpret_cast<uintptr_t>(d_m) & (align - 1u)) != 0u)) return CIERA_ERR_ARG;
@@ -831,11 +1159,15 @@ ciera_status mx_decode_impl(const void* d_q, uint64_t q_bytes, uint64_t rows, ui
   return launch_status();
 }
 
+constexpr uint32_t kMxCus = 256u;
+uint32_t mx_wgrad_parts(uint64_t tokens, uint64_t n, uint64_t k, uint64_t groups);
+
 uint64_t mx_ws_size(uint64_t tokens, uint64_t n, uint64_t k, uint64_t groups) {
   if (tokens > kMxMaxRows - 1u || !n || !k || n > kMxMaxCols || k > kMxMaxCols || !groups || groups > kMxMaxGroups ||
       groups * n > kMxMaxRows)
     return 0u;
-  return kMxWsHead;
+  const uint64_t parts = mx_wgrad_parts(tokens, n, k, groups);
+  return kMxWsHead + (parts > 1u ? parts * groups * n * k * 4u : 0u);
 }
 
 // The checks every product makes, and the arguments they share.
@@ -868,6 +1200,7 @@ ciera_status mx_product(MxArgs& p, const void* d_w, uint64_t w_bytes, void* d_ou
   p.k = uint32_t(k);
   p.kp = uint32_t(mx_pitch(k));
   p.groups = groups;
+  p.parts = 1u;
   p.out_f32 = out_f32;
   return CIERA_OK;
 }
@@ -878,20 +1211,50 @@ uint64_t mx_token_tiles(const MxArgs& p, uint32_t bm) {
   return p.tokens / bm + (p.groups < p.tokens ? p.groups : p.tokens);
 }
 
-// Few rows a group: the weights' read dominates (k_mx_few).  Otherwise tiles
-// of 256 rows, or of 64 where a group's rows would leave most of 256 empty.
-uint32_t mx_rows_per_tile(const MxArgs& p) { return p.tokens / p.groups > 96u ? 256u : 64u; }
+// Tiles of 128 rows, or of 32 where a group's rows would leave most of 128
+// empty.
+bool mx_many_rows(const MxArgs& p) { return p.tokens / p.groups > 64u; }
 
+template <int kOp, uint32_t kBM, uint32_t kBN, uint32_t kBC, uint32_t kWM, uint32_t kWN, uint32_t kStages, uint32_t kPerCu>
+ciera_status mx_gemm_as(const MxArgs& p, hipStream_t stream) {
+  constexpr bool kRowsB = kOp == kMxMatmul || kOp == kMxMatmul8;
+  const uint64_t mtiles = kOp == kMxWgrad ? cdiv(p.n, kBM) * p.groups * p.parts : mx_token_tiles(p, kBM);
+  const uint64_t grid = mtiles * cdiv(kRowsB ? p.n : p.k, kBN);
+  if (grid > 0x7FFFFFFFu) return CIERA_ERR_ARG;
+  launch(k_mx_gemm<kOp, kBM, kBN, kBC, kWM, kWN, kStages, kPerCu>, dim3(uint32_t(grid)), dim3(kWM * kWN * 64u), stream, p);
+  return launch_status();
+}
+template <uint32_t kBM, uint32_t kBN, uint32_t kWM, uint32_t kWN, uint32_t kStages, uint32_t kPerCu>
+ciera_status mx_gemm8_as(const MxArgs& p, hipStream_t stream) {
+  const uint64_t grid = mx_token_tiles(p, kBM) * cdiv(p.n, kBN);
+  if (grid > 0x7FFFFFFFu) return CIERA_ERR_ARG;
+  launch(k_mx_gemm8<kBM, kBN, kWM, kWN, kStages, kPerCu>, dim3(uint32_t(grid)), dim3(kWM * kWN * 64u), stream, p);
+  return launch_status();
+}
+
+// The tile shapes, each the fastest measured where the rule sends it.
+//   matmul  rows x 256 columns, two workgroups a CU; where that leaves CUs
+//           without a second one, columns in halves (4,001 x 2,048 x 2,048: 37
+//           against 41 us, 32,768 rows: 256 against 246 us).
+//   dx      256 x 256 once groups are long enough that a tile's empty rows do
+//           not matter (32,768 rows in one group, n = k = 2,048: 262 against
+//           282 us), else 128 rows (64 groups of 512: 187 against 200 us).
+// Few rows a group leave most of such a tile empty; tiles of 32 rows then read
+// the weights about as often and multiply a quarter as much.
 template <int kOp>
 ciera_status mx_gemm(const MxArgs& p, hipStream_t stream) {
-  const uint32_t bm = kOp == kMxWgrad ? 256u : mx_rows_per_tile(p);
-  const uint64_t ntiles = cdiv(kOp == kMxMatmul || kOp == kMxMatmul8 ? p.n : p.k, kMxBN);
-  const uint64_t mtiles = kOp == kMxWgrad ? cdiv(p.n, bm) * p.groups : mx_token_tiles(p, bm);
-  const uint64_t grid = ntiles * mtiles;
-  if (grid > 0x7FFFFFFFu) return CIERA_ERR_ARG;
-  if (bm == 256u) launch(k_mx_gemm<kOp, 256u>, dim3(uint32_t(grid)), dim3(kMxThreads), stream, p);
-  else if constexpr (kOp != kMxWgrad) launch(k_mx_gemm<kOp, 64u>, dim3(uint32_t(grid)), dim3(kMxThreads), stream, p);
-  return launch_status();
+  if constexpr (kOp == kMxDx) {
+    if (p.tokens / p.groups >= 1024u) return mx_gemm_as<kOp, 256u, 256u, 64u, 2u, 4u, 2u, 1u>(p, stream);
+    if (mx_many_rows(p)) return mx_gemm_as<kOp, 128u, 256u, 32u, 2u, 2u, 3u, 2u>(p, stream);
+    return mx_gemm_as<kOp, 32u, 256u, 32u, 1u, 4u, 6u, 2u>(p, stream);
+  } else {
+    if (mx_many_rows(p)) {
+      if (cdiv(p.tokens, 128u) * cdiv(p.n, 256u) >= 2u * kMxCus) return mx_gemm_as<kOp, 128u, 256u, 64u, 2u, 2u, 3u, 2u>(p, stream);
+      return mx_gemm_as<kOp, 128u, 128u, 64u, 2u, 2u, 2u, 3u>(p, stream);
+    }
+    if constexpr (kOp == kMxMatmul8) return mx_gemm_as<kOp, 64u, 128u, 64u, 1u, 4u, 3u, 2u>(p, stream);
+    else return mx_gemm_as<kOp, 32u, 128u, 64u, 1u, 4u, 3u, 2u>(p, stream);
+  }
 }
 
 template <bool kMx8>
@@ -907,15 +1270,36 @@ ciera_status mx_matmul_impl(MxArgs& p, hipStream_t stream) {
   }
   if constexpr (kMx8) {
     if (p.out_f32) return mx_gemm<kMxMatmul8>(p, stream);
-    const uint32_t bm = mx_rows_per_tile(p);
-    const uint64_t grid = cdiv(p.n, kMxBN) * mx_token_tiles(p, bm);
-    if (grid > 0x7FFFFFFFu) return CIERA_ERR_ARG;
-    if (bm == 256u) launch(k_mx_gemm8<256u>, dim3(uint32_t(grid)), dim3(kMxThreads), stream, p);
-    else launch(k_mx_gemm8<64u>, dim3(uint32_t(grid)), dim3(kMxThreads), stream, p);
-    return launch_status();
+    if (mx_many_rows(p)) return mx_gemm8_as<128u, 256u, 2u, 2u, 2u, 2u>(p, stream);
+    return mx_gemm8_as<32u, 128u, 1u, 4u, 3u, 2u>(p, stream);
   } else {
     return mx_gemm<kMxMatmul>(p, stream);
   }
+}
+
+// wgrad: where the tiles would leave CUs idle, each group's tokens go in up to
+// eight parts, at least 512 rows each on average, whose FP32 sums k_mx_join
+// adds in order.
+uint32_t mx_wgrad_parts(uint64_t tokens, uint64_t n, uint64_t k, uint64_t groups) {
+  const uint64_t tiles = cdiv(n, 256u) * cdiv(k, 128u) * groups;
+  uint64_t parts = 2u * kMxCus / tiles;
+  if (parts > tokens / groups / 512u) parts = tokens / groups / 512u;
+  return parts < 1u ? 1u : parts > 8u ? 8u : uint32_t(parts);
+}
+ciera_status mx_wgrad_impl(MxArgs p, hipStream_t stream) {
+  (void)hipGetLastError();
+  p.parts = mx_wgrad_parts(p.tokens, p.n, p.k, p.groups);
+  if (p.parts == 1u) return mx_gemm_as<kMxWgrad, 256u, 128u, 32u, 2u, 2u, 3u, 2u>(p, stream);
+  MxArgs sums = p;
+  sums.out = reinterpret_cast<uint8_t*>(p.ctrl) + kMxWsHead;
+  sums.out_f32 = 1u;
+  sums.accumulate = 0u;
+  const ciera_status st = mx_gemm_as<kMxWgrad, 256u, 128u, 32u, 2u, 2u, 3u, 2u>(sums, stream);
+  if (st != CIERA_OK) return st;
+  const uint64_t count = uint64_t(p.groups) * p.n * p.k;
+  launch(k_mx_join, dim3(uint32_t(cdiv(count, kMxThreads * 4u))), dim3(kMxThreads), stream, p,
+         static_cast<const float*>(sums.out), count);
+  return launch_status();
 }
 
 }  // namespace
@@ -1006,8 +1390,7 @@ ciera_status mx8_wgrad(const void* d_dy, uint64_t lddy, const void* d_xq, uint64
   p.xq = static_cast<const uint8_t*>(d_xq);
   p.xs = p.xq + mx_scales_at(tokens, k, 8u);
   p.accumulate = accumulate;
-  (void)hipGetLastError();
-  return mx_gemm<kMxWgrad>(p, stream);
+  return mx_wgrad_impl(p, stream);
 }
 
 }  // extern "C"
