@@ -1025,71 +1025,154 @@ __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_
   }
 }
 
-// matmul for few tokens a group: bound by reading the weights once.  A
-// workgroup takes 16 weight rows of a group and all the group's tokens, 16 a
-// pass; its waves take turns over the steps of 128 contraction values and
-// their sums are added in wave order at the end.  A lane reads 16 bytes, one
-// block of a weight row, straight into registers.
-constexpr uint32_t kMxFewWaves = 8u;
+// matmul for few tokens a group: bound by reading the weights once.  A wave
+// takes 16 weight rows and 16 of the group's tokens; a lane reads 16 bytes of
+// a weight row, one block, straight into registers and makes BF16 of it there,
+// 128 contraction values a step, eight steps of loads ahead.
+//   kSplit 1: the eight waves of a workgroup take 128 weight rows and share
+//             the tokens' values through LDS.
+//   kSplit 8: eight waves take the same 16 rows and every eighth step, their
+//             sums are added in wave order; for calls with too few rows to
+//             fill the chip otherwise.
+// 64 rows on 42 of 64 groups of 1,024 x 2,048: TIME us for 47 MB.
+constexpr uint32_t kMxFewThreads = 512u;
+
+// Eight values of x, c a multiple of 8: as loaded (mx8: the values, then the
+// scale byte), and as BF16.  Behind the contraction's end: zeros.
 template <bool kMx8>
-__global__ __launch_bounds__(kMxFewWaves * 64u) void k_mx_few(MxArgs p) {
-  __shared__ float s_sum[kMxFewWaves][16][16];
+__device__ __forceinline__ u32x4v mx_few_load(const MxArgs& p, uint64_t row, uint32_t c) {
+  if constexpr (kMx8) {
+    const u32x2v q = *reinterpret_cast<const u32x2v*>(p.xq + row * p.kp + c);
+    return u32x4v{q[0], q[1], p.xs[row * (p.kp / 32u) + c / 32u], 0u};
+  } else {
+    return *reinterpret_cast<const u32x4a2*>(p.a + row * p.lda + (c + 8u <= p.k ? c : 0u));
+  }
+}
+template <bool kMx8>
+__device__ __forceinline__ u32x4v mx_few_value(const MxArgs& p, u32x4v v, uint64_t row, uint32_t c) {
+  if constexpr (kMx8) return mx_unit8(v[0], v[1], mx_scale(v[2]));
+  if (c + 8u > p.k) return mx_part8(p.a + row * p.lda + (c < p.k ? c : 0u), c < p.k ? p.k - c : 0u);
+  return v;
+}
+
+template <bool kMx8, uint32_t kSplit>
+__global__ __launch_bounds__(kMxFewThreads, 4) void k_mx_few(MxArgs p) {
+  constexpr uint32_t kWaves = kMxFewThreads / 64u;
+  constexpr uint32_t kAhead = kSplit == 1u ? 8u : 4u;
+  constexpr uint32_t kPitch = kAhead * 128u + 8u;  // a row's start moves on by 16 bytes of banks
+  constexpr uint32_t kPer = kAhead * 16u;          // units of 8 values of a row
+  constexpr uint32_t kFirst = 2u;                  // units a thread fetches before the weights
+  __shared__ __attribute__((aligned(16))) uint16_t s_x[kSplit == 1u ? 16u * kPitch : 8u];
+  __shared__ float s_sum[kSplit == 1u ? 1u : kWaves][16][16];
   const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
   if (blockIdx.x == 0u && blockIdx.y == 0u) mx_report(p);
-  const uint32_t g = blockIdx.y, n0 = blockIdx.x * 16u;
+  const uint32_t g = blockIdx.y;
   uint32_t r0, r1;
   mx_rows(p, g, r0, r1);
+  if (r0 == r1) return;
+  const uint32_t n0 = kSplit == 1u ? (blockIdx.x * kWaves + wave) * 16u : blockIdx.x * 16u;
   const uint32_t l16 = lane & 15u, kb = lane >> 4;
   const uint64_t wrow = uint64_t(g) * p.n + min(n0 + l16, p.n - 1u);
   const uint8_t* wq = p.wq + wrow * (p.kp / 2u) + kb * 16u;
-  const uint8_t* ws = p.ws + wrow * (p.kp / 32u) + kb;
+  const uint8_t* ws = p.ws + wrow * (p.kp / 32u);
   const uint32_t steps = p.kp / 128u;
+  const bool some = p.k >= 8u;  // a whole unit of x exists
   for (uint32_t t0 = r0; t0 < r1; t0 += 16u) {
-    const uint64_t row = min(t0 + l16, r1 - 1u);
-    v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (uint32_t step = wave; step < steps; step += kMxFewWaves) {
-      const v4i q = *reinterpret_cast<const v4i*>(wq + step * 64u);
-      const uint32_t sb = ws[step * 4u];
-      u32x4v xv[4];
-      if constexpr (kMx8) {
-        const uint8_t* xq = p.xq + row * p.kp + step * 128u + kb * 32u;
-        const u32x4v lo = *reinterpret_cast<const u32x4v*>(xq);
-        const u32x4v hi = *reinterpret_cast<const u32x4v*>(xq + 16u);
-        const float sx = mx_scale(p.xs[row * (p.kp / 32u) + step * 4u + kb]);
-        xv[0] = mx_unit8(lo[0], lo[1], sx);
-        xv[1] = mx_unit8(lo[2], lo[3], sx);
-        xv[2] = mx_unit8(hi[0], hi[1], sx);
-        xv[3] = mx_unit8(hi[2], hi[3], sx);
-      } else {
-        const uint32_t c = step * 128u + kb * 32u;
-        const uint16_t* x = p.a + row * p.lda + c;
-        if (step * 128u + 128u <= p.k) {
+    const uint32_t have = min(16u, r1 - t0);
+    const uint32_t row = min(l16, have - 1u);
+    v4f acc[2] = {};
+    constexpr uint32_t kBy = kSplit == 1u ? 1u : kWaves;
+    for (uint32_t at = kSplit == 1u ? 0u : wave; at < steps; at += kBy * kAhead) {
+      const bool whole = at + (kAhead - 1u) * kBy < steps;
+      const uint32_t units = have * kPer;
+      u32x4v first[kFirst];
+      if constexpr (kSplit == 1u) {
 #pragma unroll
-          for (int j = 0; j < 4; j++) xv[j] = *reinterpret_cast<const u32x4a2*>(x + 8 * j);
-        } else {  // zeros behind the contraction's end
-#pragma unroll
-          for (int j = 0; j < 4; j++) {
-            const uint32_t at = c + 8u * uint32_t(j);
-            xv[j] = mx_part8(x + 8 * j, at < p.k ? p.k - at : 0u);
-          }
+        for (uint32_t i = 0; i < kFirst; i++) {
+          const uint32_t u = min(i * kMxFewThreads + tid, units - 1u);
+          const uint32_t c = min(at * 128u + u % kPer * 8u, p.kp - 8u);
+          if (kMx8 || some) first[i] = mx_few_load<kMx8>(p, t0 + u / kPer, c);
         }
       }
-      const float s = mx_scale(sb);
+      v4i q[kAhead];
+      uint32_t sb[kAhead];
 #pragma unroll
-      for (int j = 0; j < 4; j++)
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, xv[j]),
-                                                      __builtin_bit_cast(v8bf, mx_unit4(uint32_t(q[j]), s)), acc, 0, 0,
-                                                      0);
+      for (uint32_t i = 0; i < kAhead; i++)
+        q[i] = *reinterpret_cast<const v4i*>(wq + min(at + i * kBy, steps - 1u) * 64u);
+      if (kSplit == 1u && whole) {  // a word of scale bytes a step, four at a time
+#pragma unroll
+        for (uint32_t i = 0; i < kAhead; i += 4u) {
+          typedef uint32_t u32x4a4 __attribute__((ext_vector_type(4), aligned(4)));
+          const u32x4v w = *reinterpret_cast<const u32x4a4*>(ws + (at + i) * 4u);
+#pragma unroll
+          for (uint32_t j = 0; j < 4u; j++) sb[i + j] = w[j];
+        }
+      } else {
+#pragma unroll
+        for (uint32_t i = 0; i < kAhead; i++)
+          sb[i] = *reinterpret_cast<const uint32_t*>(ws + min(at + i * kBy, steps - 1u) * 4u);
+      }
+      if constexpr (kSplit == 1u) {
+        if (at) __syncthreads();
+#pragma unroll
+        for (uint32_t i = 0; i < kFirst; i++) {
+          const uint32_t u = i * kMxFewThreads + tid, c = at * 128u + u % kPer * 8u;
+          if (u < units && c < p.kp)
+            *reinterpret_cast<u32x4v*>(s_x + u / kPer * kPitch + u % kPer * 8u) =
+                mx_few_value<kMx8>(p, first[i], t0 + u / kPer, c);
+        }
+        for (uint32_t u = kFirst * kMxFewThreads + tid; u < units; u += kMxFewThreads) {
+          const uint32_t r = u / kPer, c = at * 128u + u % kPer * 8u;
+          if (c < p.kp) {
+            u32x4v v = {0u, 0u, 0u, 0u};
+            if (kMx8 || some) v = mx_few_load<kMx8>(p, t0 + r, c);
+            *reinterpret_cast<u32x4v*>(s_x + r * kPitch + u % kPer * 8u) = mx_few_value<kMx8>(p, v, t0 + r, c);
+          }
+        }
+        __syncthreads();
+      }
+      const auto take = [&](uint32_t i) {
+        const float s = mx_scale((sb[i] >> (8u * kb)) & 255u);
+#pragma unroll
+        for (uint32_t j = 0; j < 4u; j++) {
+          u32x4v x;
+          if constexpr (kSplit == 1u) {
+            x = *reinterpret_cast<const u32x4v*>(s_x + row * kPitch + i * 128u + kb * 32u + j * 8u);
+          } else {
+            const uint32_t c = (at + i * kBy) * 128u + kb * 32u + j * 8u;
+            x = u32x4v{0u, 0u, 0u, 0u};
+            if (kMx8 || some) x = mx_few_load<kMx8>(p, t0 + row, c);
+            x = mx_few_value<kMx8>(p, x, t0 + row, c);
+          }
+          acc[j & 1u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              __builtin_bit_cast(v8bf, x), __builtin_bit_cast(v8bf, mx_unit4(uint32_t(q[i][j]), s)), acc[j & 1u], 0, 0, 0);
+        }
+      };
+      if (whole) {
+#pragma unroll
+        for (uint32_t i = 0; i < kAhead; i++) take(i);
+      } else {
+#pragma unroll
+        for (uint32_t i = 0; i < kAhead; i++)
+          if (at + i * kBy < steps) take(i);
+      }
     }
+    const v4f sum = acc[0] + acc[1];
+    if constexpr (kSplit == 1u) {
 #pragma unroll
-    for (int r = 0; r < 4; r++) s_sum[wave][kb * 4u + r][l16] = acc[r];
-    __syncthreads();
-    if (tid < 256u) {
-      const uint32_t tr = tid >> 4, col = n0 + (tid & 15u);
-      float v = 0.0f;
+      for (uint32_t r = 0; r < 4u; r++)
+        if (kb * 4u + r < have && n0 + l16 < p.n) mx_store(p, uint64_t(t0 + kb * 4u + r) * p.ldo + n0 + l16, sum[r]);
+    } else {
 #pragma unroll
-      for (uint32_t w = 0; w < kMxFewWaves; w++) v += s_sum[w][tr][tid & 15u];
-      if (t0 + tr < r1 && col < p.n) mx_store(p, uint64_t(t0 + tr) * p.ldo + col, v);
+      for (uint32_t r = 0; r < 4u; r++) s_sum[wave][kb * 4u + r][l16] = sum[r];
+      __syncthreads();
+      if (tid < 256u) {
+        const uint32_t tr = tid >> 4, col = n0 + (tid & 15u);
+        float v = 0.0f;
+#pragma unroll
+        for (uint32_t w = 0; w < kWaves; w++) v += s_sum[w][tr][tid & 15u];
+        if (tr < have && col < p.n) mx_store(p, uint64_t(t0 + tr) * p.ldo + col, v);
+      }
     }
     __syncthreads();
   }
@@ -1265,7 +1348,12 @@ ciera_status mx_matmul_impl(MxArgs& p, hipStream_t stream) {
     return launch_status();
   }
   if (p.tokens <= 32u * uint64_t(p.groups)) {
-    launch(k_mx_few<kMx8>, dim3(uint32_t(cdiv(p.n, 16u)), p.groups), dim3(kMxFewWaves * 64u), stream, p);
+    // 128 rows a workgroup once that gives every CU one
+    const uint64_t live = p.groups < p.tokens ? p.groups : p.tokens;
+    if (cdiv(p.n, 128u) * live >= kMxCus)
+      launch(k_mx_few<kMx8, 1u>, dim3(uint32_t(cdiv(p.n, 128u)), p.groups), dim3(kMxFewThreads), stream, p);
+    else
+      launch(k_mx_few<kMx8, 8u>, dim3(uint32_t(cdiv(p.n, 16u)), p.groups), dim3(kMxFewThreads), stream, p);
     return launch_status();
   }
   if constexpr (kMx8) {

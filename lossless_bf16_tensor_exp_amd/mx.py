@@ -23,16 +23,18 @@ device is current runs on the tensors' own, on that device's current stream.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
 
-from . import _check_bytes, _ptr, _raise, load_library
+from . import _raise, load_library
 
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
+_f32, _i64, _u8 = torch.float32, torch.int64, torch.uint8
 _vp, _u64, _u32, _i32 = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint32, ctypes.c_int
 _bound = None
+_current_device = torch.cuda.current_device
+_current_stream = torch.cuda.current_stream
 
 
 def _lib():
@@ -62,38 +64,44 @@ def _lib():
 
 def _rows(t, name, f32=False):
     """Rows, columns and row stride of a matrix; f32: FP32 allowed too."""
-    if t.dtype not in _BF16 and not (f32 and t.dtype is torch.float32):
+    dtype = t.dtype
+    if dtype not in _BF16 and not (f32 and dtype is _f32):
         raise TypeError(f"{name} must hold BF16 patterns (bfloat16/int16/uint16){' or float32' if f32 else ''}, "
-                        f"got {t.dtype}")
+                        f"got {dtype}")
     if not t.is_cuda or t.dim() != 2:
         raise ValueError(f"{name} must be a two-dimensional device tensor")
     rows, cols = t.shape
-    ld = t.stride(0) if rows > 1 else cols
-    if (cols > 1 and t.stride(1) != 1) or ld < cols:
+    ld, step = t.stride()
+    if rows <= 1:
+        ld = cols
+    if (step != 1 and cols > 1) or ld < cols:
         raise ValueError(f"{name}'s rows must be contiguous and must not overlap")
     return rows, cols, ld
 
 
-def _same_device(t, *others):
+def _bytes(t, name):
+    """Address and length of a buffer of bytes."""
+    if t.dtype is not _u8 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous uint8 device tensor")
+    n = t.numel()
+    return (t.data_ptr() if n else None), n
+
+
+def _call(name, device, others, stream, *args):
+    """The C call ``name`` on the tensors' device: the current stream there
+    unless one is given."""
     for o in others:
-        if o is not None and o.device != t.device:
-            raise ValueError(f"tensors on {t.device} and {o.device} in one call")
-
-
-class _On:
-    """The device of t made current, and the stream to launch on."""
-
-    def __init__(self, t, stream):
-        index = t.device.index
-        self.guard = contextlib.nullcontext() if index == torch.cuda.current_device() else torch.cuda.device(index)
-        self.stream = torch.cuda.current_stream(index).cuda_stream if stream is None else stream.cuda_stream
-
-    def __enter__(self):
-        self.guard.__enter__()
-        return self.stream
-
-    def __exit__(self, *exc):
-        return self.guard.__exit__(*exc)
+        if o.get_device() != device:
+            raise ValueError(f"tensors on cuda:{device} and {o.device} in one call")
+    f = getattr(_lib(), name)
+    s = (_current_stream(device) if stream is None else stream).cuda_stream
+    if device == _current_device():
+        st = f(*args, s)
+    else:
+        with torch.cuda.device(device):
+            st = f(*args, s)
+    if st:
+        _raise(st, name)
 
 
 def mx8_encoded_size(rows: int, cols: int) -> int:
@@ -109,23 +117,15 @@ def mx_workspace_size(tokens: int, n: int, k: int, groups: int = 1) -> int:
 
 
 def _encode(name, x, out, stream):
-    lib = _lib()
     rows, cols, ld = _rows(x, "x")
-    _check_bytes(out, "out")
-    _same_device(x, out)
-    with _On(x, stream) as s:
-        st = getattr(lib, name)(x.data_ptr(), rows, cols, ld, _ptr(out), out.numel(), s)
-    _raise(st, name)
+    to, size = _bytes(out, "out")
+    _call(name, x.get_device(), (out,), stream, x.data_ptr(), rows, cols, ld, to, size)
 
 
 def _decode(name, inp, y, stream):
-    lib = _lib()
     rows, cols, ld = _rows(y, "y")
-    _check_bytes(inp, "inp")
-    _same_device(y, inp)
-    with _On(y, stream) as s:
-        st = getattr(lib, name)(_ptr(inp), inp.numel(), rows, cols, y.data_ptr(), ld, s)
-    _raise(st, name)
+    src, size = _bytes(inp, "inp")
+    _call(name, y.get_device(), (inp,), stream, src, size, rows, cols, y.data_ptr(), ld)
 
 
 def mx8_encode(x, out, stream=None) -> None:
@@ -150,30 +150,26 @@ def mx4_decode(inp, y, stream=None) -> None:
     _decode("mx4_decode", inp, y, stream)
 
 
-def _groups(offsets, device_of):
+def _groups(offsets):
+    """Number of groups, the table's address, and the table among the tensors of the call."""
     if offsets is None:
-        return 1, None
-    if offsets.dtype is not torch.int64 or not offsets.is_cuda or not offsets.is_contiguous() or offsets.numel() < 2:
+        return 1, None, ()
+    if offsets.dtype is not _i64 or not offsets.is_cuda or not offsets.is_contiguous() or offsets.numel() < 2:
         raise ValueError("offsets must be a contiguous int64 device tensor of groups + 1 row numbers")
-    _same_device(device_of, offsets)
-    return offsets.numel() - 1, offsets.data_ptr()
+    return offsets.numel() - 1, offsets.data_ptr(), (offsets,)
 
 
 def _product(name, a, lead, width, w, out, ws, offsets, tokens, n, k, stream):
     """One call of a matmul-shaped entry point; ``lead`` is its left operand's
     pointer and stride or size, ``width`` the output's columns."""
-    lib = _lib()
     rows, cols, ldo = _rows(out, "the output", f32=True)
     if rows != tokens or cols != width:
         raise ValueError(f"the output is {rows} x {cols}, the product {tokens} x {width}")
-    _check_bytes(w, "w")
-    _check_bytes(ws, "ws")
-    _same_device(out, a, w, ws)
-    groups, offs = _groups(offsets, out)
-    with _On(out, stream) as s:
-        st = getattr(lib, name)(*lead, _ptr(w), w.numel(), out.data_ptr(), ldo, int(out.dtype is torch.float32), tokens,
-                                n, k, groups, offs, _ptr(ws), ws.numel(), s)
-    _raise(st, name)
+    wp, wn = _bytes(w, "w")
+    sp, sn = _bytes(ws, "ws")
+    groups, offs, table = _groups(offsets)
+    _call(name, out.get_device(), (a, w, ws, *table), stream, *lead, wp, wn, out.data_ptr(), ldo,
+          1 if out.dtype is _f32 else 0, tokens, n, k, groups, offs, sp, sn)
 
 
 def mx4_matmul(x, w, y, ws, offsets=None, stream=None) -> None:
@@ -186,9 +182,10 @@ def mx4_matmul(x, w, y, ws, offsets=None, stream=None) -> None:
 
 def mx4_matmul_mx8(xq, k: int, w, y, ws, offsets=None, stream=None) -> None:
     """y = x W^T with x (y's rows, k) in mx8."""
-    _check_bytes(xq, "xq")
+    if y.dim() != 2:
+        raise ValueError("the output must be a two-dimensional device tensor")
     tokens, n = y.shape
-    _product("mx4_matmul_mx8", xq, (_ptr(xq), xq.numel()), n, w, y, ws, offsets, tokens, n, k, stream)
+    _product("mx4_matmul_mx8", xq, _bytes(xq, "xq"), n, w, y, ws, offsets, tokens, n, k, stream)
 
 
 def mx4_matmul_dx(dy, w, dx, ws, offsets=None, stream=None) -> None:
@@ -202,18 +199,14 @@ def mx8_wgrad(dy, xq, dw, ws, offsets=None, accumulate: bool = False, stream=Non
     """dW = dy^T x per group: dy (tokens, n) BF16, xq the (tokens, k) mx8
     checkpoint of x, dw (groups, n, k), or (n, k) for one group, contiguous,
     BF16 or float32; accumulate adds to dw instead of writing it."""
-    lib = _lib()
     tokens, n, ld = _rows(dy, "dy")
-    groups, offs = _groups(offsets, dy)
-    if dw.dtype not in _BF16 and dw.dtype is not torch.float32:
+    groups, offs, table = _groups(offsets)
+    if dw.dtype not in _BF16 and dw.dtype is not _f32:
         raise TypeError(f"dw must hold BF16 patterns (bfloat16/int16/uint16) or float32, got {dw.dtype}")
     shape = tuple(dw.shape) if dw.dim() == 3 else (1, *dw.shape)
     if not dw.is_cuda or not dw.is_contiguous() or len(shape) != 3 or shape[:2] != (groups, n):
         raise ValueError(f"dw must be a contiguous device tensor ({groups}, {n}, k), got {tuple(dw.shape)}")
-    _check_bytes(xq, "xq")
-    _check_bytes(ws, "ws")
-    _same_device(dy, xq, dw, ws)
-    with _On(dy, stream) as s:
-        st = lib.mx8_wgrad(dy.data_ptr(), ld, _ptr(xq), xq.numel(), dw.data_ptr(), int(dw.dtype is torch.float32),
-                           int(accumulate), tokens, n, shape[2], groups, offs, _ptr(ws), ws.numel(), s)
-    _raise(st, "mx8_wgrad")
+    xp, xn = _bytes(xq, "xq")
+    sp, sn = _bytes(ws, "ws")
+    _call("mx8_wgrad", dy.get_device(), (xq, dw, ws, *table), stream, dy.data_ptr(), ld, xp, xn, dw.data_ptr(),
+          1 if dw.dtype is _f32 else 0, 1 if accumulate else 0, tokens, n, shape[2], groups, offs, sp, sn)
