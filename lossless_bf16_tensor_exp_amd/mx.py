@@ -34,7 +34,8 @@ _f32, _i64, _u8 = torch.float32, torch.int64, torch.uint8
 _vp, _u64, _u32, _i32 = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint32, ctypes.c_int
 _bound = None
 _current_device = torch.cuda.current_device
-_current_stream = torch.cuda.current_stream
+# the current stream's handle without the Stream object around it (1 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
 def _lib():
@@ -94,7 +95,7 @@ def _call(name, device, others, stream, *args):
         if o.get_device() != device:
             raise ValueError(f"tensors on cuda:{device} and {o.device} in one call")
     f = getattr(_lib(), name)
-    s = (_current_stream(device) if stream is None else stream).cuda_stream
+    s = _raw_stream(device) if stream is None else stream.cuda_stream
     if device == _current_device():
         st = f(*args, s)
     else:
