@@ -436,7 +436,8 @@ ciera_status ciera_encode_ex(const void* d_x, uint64_t n, uint32_t B, uint8_t* d
  * d_offsets: groups + 1 int64 on the device, not decreasing, within 0..tokens;
  * null (one group only) stands for {0, tokens}.  A pair that decreases or
  * leaves 0..tokens holds no rows, and ciera_read_error(d_ws) then reports
- * CIERA_ERR_ARG.
+ * CIERA_ERR_ARG; nothing outside the matrices is touched, but no row of the
+ * output can be relied on.
  *
  * Sums are held in FP32 and rounded once, to nearest, when the output is
  * BF16, with one exception: mx4_matmul_mx8 with a BF16 output may take a block's

@@ -414,7 +414,6 @@ __device__ __forceinline__ void mx_store_frag(const MxArgs& p, bool row_ok, uint
 
 enum MxOp { kMxMatmul = 0, kMxDx = 1, kMxWgrad = 2, kMxMatmul8 = 3 };
 
-
 // Loads from global memory straight into LDS: lane i's 16 (or 4) bytes at
 // base + off land at lds + 16 i (4 i).  No register holds them, so they stay
 // in flight over whole steps; mx_fence counts them.
@@ -1041,8 +1040,16 @@ __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_
 //   kSplit 8: eight waves take the same 16 rows and every eighth step, their
 //             sums are added in wave order; for calls with too few rows to
 //             fill the chip otherwise.
-// 64 rows on 42 of 64 groups of 1,024 x 2,048: TIME us for 47 MB.
+// 64 rows on 42 of 64 groups of 1,024 x 2,048: 13.3 us for 47 MB, 3.5 TB/s;
+// one row, n = k = 2,048: 6.9 us, a launch.  Its time grows with the outputs,
+// the tiles' does not until they fill the chip: taken up to kMxFewOutputs (16
+// rows, n = 2,048: 7.9 against 12.5 us; 32 rows: 9.6 against 12.5; 8 rows, n =
+// 16,384: 12.7 against 12.9; 16 rows: 15.7 against 13.0; 64 groups, n = 1,024,
+// 128 rows: 16.5 against 17.6, 512 rows: 25 against 18).  x in mx8 with a BF16
+// result goes to the scaled instructions at any size (n = 2,048, one row: 8.8
+// against 8.3 us; 64 rows in 64 groups: 13.4 against 16.3).
 constexpr uint32_t kMxFewThreads = 512u;
+constexpr uint64_t kMxFewOutputs = 1u << 17;  // the most outputs (all tokens' n) for which it is taken
 
 // Eight values of x, c a multiple of 8: as loaded (mx8: the values, then the
 // scale byte), and as BF16.  Behind the contraction's end: zeros.
@@ -1301,9 +1308,10 @@ uint64_t mx_token_tiles(const MxArgs& p, uint32_t bm) {
   return p.tokens / bm + (p.groups < p.tokens ? p.groups : p.tokens);
 }
 
-// Tiles of 128 rows, or of 32 where a group's rows would leave most of 128
-// empty.
-bool mx_many_rows(const MxArgs& p) { return p.tokens / p.groups > 64u; }
+// What the rules below go by: tiles of 128 x 256 that the output would make,
+// and the rows a group has on average.
+uint64_t mx_tiles(const MxArgs& p, uint64_t cols) { return cdiv(p.tokens, 128u) * cdiv(cols, 256u); }
+uint32_t mx_rows_each(const MxArgs& p) { return p.tokens / p.groups; }
 
 template <int kOp, uint32_t kBM, uint32_t kBN, uint32_t kBC, uint32_t kWM, uint32_t kWN, uint32_t kStages, uint32_t kPerCu>
 ciera_status mx_gemm_as(const MxArgs& p, hipStream_t stream) {
@@ -1322,29 +1330,42 @@ ciera_status mx_gemm8_as(const MxArgs& p, hipStream_t stream) {
   return launch_status();
 }
 
-// The tile shapes, each the fastest measured where the rule sends it.
-//   matmul  rows x 256 columns, two workgroups a CU; where that leaves CUs
-//           without a second one, columns in halves (4,001 x 2,048 x 2,048: 37
-//           against 41 us, 32,768 rows: 256 against 246 us).
-//   dx      256 x 256 once groups are long enough that a tile's empty rows do
-//           not matter (32,768 rows in one group, n = k = 2,048: 262 against
-//           282 us), else 128 rows (64 groups of 512: 187 against 200 us).
-// Few rows a group leave most of such a tile empty; tiles of 32 rows then read
-// the weights about as often and multiply a quarter as much.
+// The tile shapes.  Small outputs want many small tiles, so that every CU has
+// work; large ones want large tiles, which read less; and a group's last tile
+// is half empty, so tiles stay below the rows a group has.  Both sides of each
+// rule, in us (rows of one group with n = k = 2,048; "8 g", "64 g": rows of so
+// many groups together with n = 1,024, k = 2,048):
+//   matmul  32 or 64 rows: 1,024: 18.0, 18.7; 2,048: 34, 25; 2,000 in 64 g: 25, 27.5; 5,000 in 64 g: 47, 40.
+//           64 or 128 rows: 3,000: 32, 34; 4,096: 46, 37; 6,000 in 64 g: 43, 46; 8,192 in 64 g: 55, 48.
+//           128 rows, 128 or 256 columns: 4,001: 37, 41; 8,192: 72, 69; 32,768: 265, 252.
+//           x in mx8, BF16 result (the scaled instructions), 32 or 64 rows: 2,048: 21, 16; 2,000 in 64 g: 17.5, 23;
+//           6,000 in 64 g: 32, 29; 64 or 128 rows: 3,000: 24, 24; 8,192: 56, 44; 6,000 in 64 g: 29, 34.
+//   dx      64 x 128 or 64 x 256: 40: 25, 42; 1,024 in 8 g: 19, 25; 1,000 in 64 g: 36, 31; 4,000 in 64 g: 53, 51.
+//           64 or 128 rows: 8,192 in 64 g: 78, 66; 32,768 in 64 g: 242, 187.
+//           128 or 256 rows: 8,192: 85, 76; 32,768: 296, 273; 16,384 in 32 g: 103, 103; 65,536 in 32 g: 332, 317.
 template <int kOp>
 ciera_status mx_gemm(const MxArgs& p, hipStream_t stream) {
   if constexpr (kOp == kMxDx) {
-    if (p.tokens / p.groups >= 1024u) return mx_gemm_as<kOp, 256u, 256u, 64u, 2u, 4u, 2u, 1u>(p, stream);
-    if (mx_many_rows(p)) return mx_gemm_as<kOp, 128u, 256u, 32u, 2u, 2u, 3u, 2u>(p, stream);
-    return mx_gemm_as<kOp, 32u, 256u, 32u, 1u, 4u, 6u, 2u>(p, stream);
+    const uint64_t tiles = mx_tiles(p, p.k);
+    if (mx_rows_each(p) >= 1024u && tiles >= 2u * kMxCus) return mx_gemm_as<kOp, 256u, 256u, 64u, 2u, 4u, 2u, 1u>(p, stream);
+    if (mx_rows_each(p) > 96u && mx_token_tiles(p, 64u) * cdiv(p.k, 256u) > 2u * kMxCus)
+      return mx_gemm_as<kOp, 128u, 256u, 32u, 2u, 2u, 3u, 2u>(p, stream);
+    if (mx_token_tiles(p, 64u) * cdiv(p.k, 128u) <= 2u * kMxCus) return mx_gemm_as<kOp, 64u, 128u, 64u, 1u, 4u, 3u, 2u>(p, stream);
+    return mx_gemm_as<kOp, 64u, 256u, 32u, 1u, 4u, 4u, 2u>(p, stream);
   } else {
-    if (mx_many_rows(p)) {
-      if (cdiv(p.tokens, 128u) * cdiv(p.n, 256u) >= 2u * kMxCus) return mx_gemm_as<kOp, 128u, 256u, 64u, 2u, 2u, 3u, 2u>(p, stream);
-      return mx_gemm_as<kOp, 128u, 128u, 64u, 2u, 2u, 2u, 3u>(p, stream);
-    }
-    if constexpr (kOp == kMxMatmul8) return mx_gemm_as<kOp, 64u, 128u, 64u, 1u, 4u, 3u, 2u>(p, stream);
-    else return mx_gemm_as<kOp, 32u, 128u, 64u, 1u, 4u, 3u, 2u>(p, stream);
+    const uint64_t tiles = mx_tiles(p, p.n);
+    if (mx_rows_each(p) > 64u && tiles >= 2u * kMxCus) return mx_gemm_as<kOp, 128u, 256u, 64u, 2u, 2u, 3u, 2u>(p, stream);
+    if (mx_rows_each(p) > 64u && tiles > 3u * kMxCus / 4u) return mx_gemm_as<kOp, 128u, 128u, 64u, 2u, 2u, 2u, 3u>(p, stream);
+    if constexpr (kOp == kMxMatmul)
+      if (mx_rows_each(p) <= 48u || tiles <= kMxCus / 4u) return mx_gemm_as<kOp, 32u, 128u, 64u, 1u, 4u, 3u, 2u>(p, stream);
+    return mx_gemm_as<kOp, 64u, 128u, 64u, 1u, 4u, 3u, 2u>(p, stream);
   }
+}
+ciera_status mx_gemm8(const MxArgs& p, hipStream_t stream) {
+  const uint64_t tiles = mx_tiles(p, p.n);
+  if (mx_rows_each(p) > 64u && tiles > 3u * kMxCus / 4u) return mx_gemm8_as<128u, 256u, 2u, 2u, 2u, 2u>(p, stream);
+  if (mx_rows_each(p) > 48u && tiles > kMxCus / 4u) return mx_gemm8_as<64u, 128u, 1u, 4u, 3u, 2u>(p, stream);
+  return mx_gemm8_as<32u, 128u, 1u, 4u, 3u, 2u>(p, stream);
 }
 
 template <bool kMx8>
@@ -1354,27 +1375,25 @@ ciera_status mx_matmul_impl(MxArgs& p, hipStream_t stream) {
     launch(k_mx_status, dim3(1), dim3(64), stream, p);
     return launch_status();
   }
-  if (p.tokens <= 32u * uint64_t(p.groups)) {
-    // 128 rows a workgroup once that gives every CU one
+  if (kMx8 && !p.out_f32) return mx_gemm8(p, stream);
+  if (uint64_t(p.tokens) * p.n <= kMxFewOutputs) {
+    // 128 rows a workgroup once that gives every other CU one (one token,
+    // k = 2,048: n = 8,192: 9.0 against 8.2 us, 16,384: 8.8 against 11.0)
     const uint64_t live = p.groups < p.tokens ? p.groups : p.tokens;
-    if (cdiv(p.n, 128u) * live >= kMxCus)
+    if (cdiv(p.n, 128u) * live >= kMxCus / 2u)
       launch(k_mx_few<kMx8, 1u>, dim3(uint32_t(cdiv(p.n, 128u)), p.groups), dim3(kMxFewThreads), stream, p);
     else
       launch(k_mx_few<kMx8, 8u>, dim3(uint32_t(cdiv(p.n, 16u)), p.groups), dim3(kMxFewThreads), stream, p);
     return launch_status();
   }
-  if constexpr (kMx8) {
-    if (p.out_f32) return mx_gemm<kMxMatmul8>(p, stream);
-    if (mx_many_rows(p)) return mx_gemm8_as<128u, 256u, 2u, 2u, 2u, 2u>(p, stream);
-    return mx_gemm8_as<32u, 128u, 1u, 4u, 3u, 2u>(p, stream);
-  } else {
-    return mx_gemm<kMxMatmul>(p, stream);
-  }
+  return mx_gemm<kMx8 ? kMxMatmul8 : kMxMatmul>(p, stream);
 }
 
 // wgrad: where the tiles would leave CUs idle, each group's tokens go in up to
 // eight parts, at least 512 rows each on average, whose FP32 sums k_mx_join
-// adds in order.
+// adds in order (n = k = 2,048, FP32: 8,192 rows 100 against 185 us in one
+// part, 2,048 rows 47 against 55; 1,024 rows in parts of 256: 38 against 33 in
+// one).
 uint32_t mx_wgrad_parts(uint64_t tokens, uint64_t n, uint64_t k, uint64_t groups) {
   const uint64_t tiles = cdiv(n, 256u) * cdiv(k, 128u) * groups;
   uint64_t parts = 2u * kMxCus / tiles;
