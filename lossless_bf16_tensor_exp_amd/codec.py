@@ -1,5 +1,6 @@
 """Buffer owners for the C ABI: allocate the stream, workspace, size slot and
-exponent caches once with torch, then call the library on them.
+exponent caches once with torch, then call the library on them.  ``MxLinear``
+does the same for a linear layer on microscaled matrices.
 
 Allocation happens only in the constructors; ``encode``/``decode`` only pass
 pointers.
@@ -9,8 +10,9 @@ from __future__ import annotations
 import torch
 
 from . import (CieraError, ciera_decode, ciera_encode, ciera_encode_e0, ciera_encode_spec, ciera_max_encoded_size,
-               ciera_read_error, ciera_workspace_size, zip3_decode, zip3_encode, zip3_encode_e0, zip3_encode_spec,
-               zip3_max_encoded_size, zip3_workspace_size)
+               ciera_read_error, ciera_workspace_size, mx4_encode, mx4_encoded_size, mx4_matmul, mx4_matmul_dx,
+               mx4_matmul_mx8, mx8_encode, mx8_encoded_size, mx8_wgrad, mx_workspace_size, zip3_decode, zip3_encode,
+               zip3_encode_e0, zip3_encode_spec, zip3_max_encoded_size, zip3_workspace_size)
 
 
 class Zip3Codec:
@@ -94,6 +96,75 @@ class CieraCodec:
     def decode_error(self, stream=None) -> int:
         """Device status of the last decode."""
         return ciera_read_error(self.ws_dec, stream)
+
+
+class MxLinear:
+    """y = x W^T with the weights in 4 bits, and its gradients from an 8-bit
+    checkpoint of x: one linear layer, or with ``offsets`` (groups + 1 row
+    numbers) the experts of a mixture-of-experts layer, whose groups (n, k)
+    matrices lie one behind the other.  Takes up to ``tokens`` rows a call.
+
+    ``keep`` and the calls that read the checkpoint share one buffer, so one
+    layer's forward and backward belong to one stream, or are ordered by the
+    caller.  ``backward`` takes the offsets its ``keep`` had."""
+
+    def __init__(self, tokens: int, n: int, k: int, groups: int = 1, device="cuda"):
+        self.tokens, self.n, self.k, self.groups = tokens, n, k, groups
+        size = mx_workspace_size(tokens, n, k, groups)
+        if size == 0:
+            raise ValueError(f"no workspace for {tokens} x {n} x {k} in {groups} groups")
+        self.w = torch.empty(mx4_encoded_size(groups * n, k), dtype=torch.uint8, device=device)
+        self.xq = torch.empty(mx8_encoded_size(tokens, k), dtype=torch.uint8, device=device)
+        self.ws = torch.empty(size, dtype=torch.uint8, device=device)
+        self.kept = 0
+
+    def load(self, weights, stream=None):
+        """The BF16 weights, (n, k) or (groups, n, k), into ``w``."""
+        rows = weights.reshape(-1, weights.shape[-1]) if weights.is_contiguous() else weights
+        if tuple(rows.shape) != (self.groups * self.n, self.k):
+            raise ValueError(f"weights are {tuple(weights.shape)}, the layer's ({self.groups}, {self.n}, {self.k})")
+        mx4_encode(rows, self.w, stream)
+
+    def _rows(self, rows: int):
+        if rows > self.tokens:
+            raise ValueError(f"{rows} rows in a layer made for {self.tokens}")
+
+    def _table(self, offsets):
+        if (1 if offsets is None else offsets.numel() - 1) != self.groups:
+            raise ValueError(f"offsets must hold {self.groups} + 1 row numbers")
+
+    def forward(self, x, y, offsets=None, stream=None):
+        """y = x W^T; nothing is kept."""
+        self._rows(x.shape[0])
+        self._table(offsets)
+        mx4_matmul(x, self.w, y, self.ws, offsets, stream)
+
+    def keep(self, x, y, offsets=None, stream=None):
+        """The checkpoint of x into ``xq``, and y from it: what ``backward``
+        sees is what the product took."""
+        self._rows(x.shape[0])
+        self._table(offsets)
+        if tuple(x.shape) != (y.shape[0], self.k):
+            raise ValueError(f"x is {tuple(x.shape)}, the product's ({y.shape[0]}, {self.k})")
+        mx8_encode(x, self.xq, stream)
+        mx4_matmul_mx8(self.xq, self.k, self.w, y, self.ws, offsets, stream)
+        self.kept = x.shape[0]
+
+    def backward(self, dy, dx, dw, offsets=None, accumulate: bool = False, stream=None):
+        """dx = dy W and dw = dy^T x from the checkpoint that ``keep`` left;
+        either output may be None."""
+        self._table(offsets)
+        if dy.shape[0] != self.kept:
+            raise ValueError(f"{dy.shape[0]} rows of dy for a checkpoint of {self.kept}")
+        if dx is not None:
+            mx4_matmul_dx(dy, self.w, dx, self.ws, offsets, stream)
+        if dw is not None:
+            mx8_wgrad(dy, self.xq, dw, self.ws, offsets, accumulate, stream)
+
+    def error(self, stream=None) -> int:
+        """Status of the last product (CIERA_ERR_ARG for offsets that are not
+        in order); synchronises."""
+        return ciera_read_error(self.ws, stream)
 
 
 # One-shot calls: allocate the stream and workspace with torch, run one
