@@ -18,6 +18,7 @@
 
 namespace {
 
+typedef int v2i __attribute__((ext_vector_type(2)));
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
@@ -412,6 +413,66 @@ __device__ __forceinline__ void mx_store_frag(const MxArgs& p, bool row_ok, uint
   }
 }
 
+// The sums of two fragments whose columns alternate, col0 + 2 c and col0 + 2 c
+// + 1: a lane's four neighbours of both are eight columns in a row.
+__device__ __forceinline__ void mx_store_pair(const MxArgs& p, uint64_t row_at, uint32_t col0, uint32_t cols,
+                                              const v16f& even, const v16f& odd) {
+#pragma unroll
+  for (int q = 0; q < 16; q += 4) {
+    const uint32_t col = col0 + 4u * uint32_t(q) + 8u * ((threadIdx.x >> 5) & 1u);
+    const v4f lo{even[q], odd[q], even[q + 1], odd[q + 1]}, hi{even[q + 2], odd[q + 2], even[q + 3], odd[q + 3]};
+    const uint64_t at = row_at + col;
+    if (col + 8u <= cols) {
+      if (p.out_f32 || p.accumulate) {
+        mx_store4(p, at, lo);
+        mx_store4(p, at + 4u, hi);
+      } else {
+        *reinterpret_cast<u32x4a2*>(static_cast<uint16_t*>(p.out) + at) =
+            u32x4v{mx_bf16x2(lo[0], lo[1]), mx_bf16x2(lo[2], lo[3]), mx_bf16x2(hi[0], hi[1]), mx_bf16x2(hi[2], hi[3])};
+      }
+    } else {
+#pragma unroll
+      for (uint32_t i = 0; i < 7u; i++)
+        if (col + i < cols) mx_store(p, at + i, i < 4u ? lo[i] : hi[i - 4u]);
+    }
+  }
+}
+
+// Eight contraction rows of two neighbouring columns as BF16.  q holds both
+// columns' values of row t in byte t (mx4) or 16-bit half t (mx8), w the rows'
+// scale bytes, each in a word that `turn` rotates to bring it to bit 23.  The
+// conversion takes its scale from the exponent bits alone and converts a row's
+// two values together; neighbouring rows are then paired column by column.
+template <int kBits>
+__device__ __forceinline__ void mx_pairs(const uint32_t (&q)[kBits / 2], u32x4v w0, u32x4v w1, uint32_t turn,
+                                         v8bf& even, v8bf& odd) {
+  u32x4v e, o;
+#pragma unroll
+  for (int t = 0; t < 8; t += 2) {
+    uint32_t v[2];
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const uint32_t w = t < 4 ? w0[t + i] : w1[t + i - 4];
+      const float s = __uint_as_float(__builtin_amdgcn_alignbit(w, w, turn));
+      v2bf b;
+      if constexpr (kBits == 8) {
+        b = i ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[t / 2], s, true)
+              : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q[t / 2], s, false);
+      } else {
+        b = t % 4 ? (i ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q[t / 4], s, 3)
+                       : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q[t / 4], s, 2))
+                  : (i ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q[t / 4], s, 1)
+                       : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q[t / 4], s, 0));
+      }
+      v[i] = __builtin_bit_cast(uint32_t, b);
+    }
+    e[t / 2] = __builtin_amdgcn_perm(v[1], v[0], 0x05040100u);
+    o[t / 2] = __builtin_amdgcn_perm(v[1], v[0], 0x07060302u);
+  }
+  even = __builtin_bit_cast(v8bf, e);
+  odd = __builtin_bit_cast(v8bf, o);
+}
+
 enum MxOp { kMxMatmul = 0, kMxDx = 1, kMxWgrad = 2, kMxMatmul8 = 3 };
 
 // Loads from global memory straight into LDS: lane i's 16 (or 4) bytes at
@@ -451,6 +512,16 @@ __device__ __forceinline__ uint32_t mx_at(uint32_t r, uint32_t chunk) {
 // piece is exclusive-ored with c, so the four rows a transposing read gathers
 // differ in bank, and the chunk within it with c / 4, for the writers.
 __device__ __forceinline__ uint32_t mx_turn_cols(uint32_t c) { return ((c & 3u) << 2) ^ ((c >> 2) & 3u); }
+
+// The mx operand of dx and wgrad, read transposed two columns at a time: what
+// 32 lanes gather, 8 rows x 32 bytes (dx) or 4 rows x 64 bytes (wgrad), covers
+// the 64 banks once.
+template <int kBits, uint32_t kRow>
+__device__ __forceinline__ uint32_t mx_turn_pairs(uint32_t r) {
+  static_assert(kRow == 128u || kRow == (kBits == 4 ? 64u : 256u), "tiles of 128 or 256 columns");
+  if (kBits == 8) return kRow == 128u ? (r >> 1 & 1u) << 2 : (r & 3u) << 2;
+  return kRow == 128u ? (r >> 1 & 3u) << 1 : (r >> 2 & 1u) << 1;
+}
 
 // Eight contraction values c0 .. c0 + 7 (c0 a multiple of 8) of one column per
 // lane: two reads that each transpose 4 rows x 16 columns within 16 lanes.
@@ -493,7 +564,6 @@ __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_
   constexpr uint32_t kStage = kABytes + kRawBytes + 4u * kScaleWords;
   // matmul: 16 scale bytes of every row at a time, eight steps' worth, twice
   constexpr uint32_t kScaleRows = kRowsB ? kBN + (kOp == kMxMatmul8 ? kBM : 0u) : 0u;
-  constexpr uint32_t kTile = kRowsB ? 0u : kBN * kBC * 2u;                      // B in BF16
   constexpr uint32_t kFM = kBM / kWM / 32u, kFN = kBN / kWN / 32u;              // 32 x 32 sums of a wave
   constexpr uint32_t kSub = kBC / 16u;                                          // matrix instructions along a step
   constexpr uint32_t kALoads = kABytes / 1024u, kRawLoads = kRawBytes / 1024u;  // of all waves; fewer than waves: some repeat
@@ -504,7 +574,8 @@ __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_
   static_assert(kRawLoads * 1024u == kRawBytes && (kRawLoads < kW ? kW % kRawLoads == 0u : kRawLoads % kW == 0u), "whole loads");
   static_assert(kScaleWords <= 64u * kW && kScaleRows % 64u == 0u, "whole waves");
   static_assert(!kRowsB || kBC == 64u, "a lane half takes a block of 32");
-  __shared__ __attribute__((aligned(256))) uint8_t lds[kStages * kStage + 2u * kTile + 32u * kScaleRows];
+  static_assert(kRowsB || (kBN / kWN % 64u == 0u && (kBN / kWN <= 128u)), "pairs of columns, one scale word a row");
+  __shared__ __attribute__((aligned(256))) uint8_t lds[kStages * kStage + 32u * kScaleRows];
   const uint32_t tid = threadIdx.x, lane = tid & 63u, half = lane >> 5;
   const uint32_t wave = mx_first(tid >> 6);
   if (blockIdx.x == 0u) mx_report(p);
@@ -617,12 +688,12 @@ __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_
       const uint32_t pos = (i * kW + wave) % kRawLoads * 64u + lane, r = pos / kRawPer;
       b_row[i] = r;
       if constexpr (kRowsB) b_off[i] = min(r, p.n - 1u - n0) * b_pitch + (pos % kRawPer) * 16u;
-      else b_off[i] = min(n0 * kBBits / 8u + ((pos % kRawPer) ^ mx_turn<kRawRow>(r)) * 16u, b_pitch - 16u);
+      else
+        b_off[i] = min(n0 * kBBits / 8u + ((pos % kRawPer) ^ mx_turn_pairs<int(kBBits), kRawRow>(r)) * 16u, b_pitch - 16u);
     }
     if constexpr (!kRowsB) {
-      constexpr uint32_t kWords = kBN / 128u;
-      bs_row = tid / kWords;
-      bs_off = min(n0 / 32u + (tid % kWords) * 4u, s_pitch - 4u);
+      bs_row = tid % kBC;  // word by word, a step's rows behind each other
+      bs_off = min(n0 / 32u + tid / kBC * 4u, s_pitch - 4u);
     }
   }
   // matmul: bytes from the scales of a row of W (r < kBN) or x to the end of
@@ -664,61 +735,22 @@ __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_
       for (uint32_t i = 0; i < kDmaRaw; i++) mx_dma16(b_off[i], b_next, at + (i * kW + wave) % kRawLoads * 1024u);
       b_next += kRawRow;
     } else {
-      // rows behind the contraction's end are fetched from its last; past the
-      // last step the load repeats it, so that every batch counts the same
+      // rows behind the contraction's end are fetched from its last
       const uint32_t last = min(c1 - 1u - step * kBC, kBC - 1u);
 #pragma unroll
       for (uint32_t i = 0; i < kDmaRaw; i++)
         mx_dma16(min(b_row[i], last) * b_pitch + b_off[i], b_next, at + (i * kW + wave) % kRawLoads * 1024u);
       if (wave * 64u < kScaleWords)
         mx_dma4(min(bs_row, last) * s_pitch + bs_off, bs_next, at + kRawBytes + wave * 256u);
-      if (step + 1u < steps) {
-        b_next += uint64_t(kBC) * b_pitch;
-        bs_next += uint64_t(kBC) * s_pitch;
-      }
-    }
-  };
-
-  // The mx operand of a step as BF16.  A thread takes 8-byte units (8 values
-  // of mx8, 16 of mx4) of one contraction row, lanes next to each other in
-  // neighbouring rows.
-  constexpr uint32_t kUnits = kTile ? kRawBytes / (512u * kW) : 1u;
-  constexpr uint32_t kPer = 8u / kBBits;  // 16-byte pieces of BF16 in a unit
-  const uint32_t raw_row = tid % kBC;
-  u32x2v raw[kUnits];
-  float raw_s[kUnits];
-  const auto raw_read = [&](uint32_t step, uint32_t slot) {
-    const uint8_t* q = lds + slot * kStage + kABytes;
-#pragma unroll
-    for (uint32_t i = 0; i < kUnits; i++) {
-      const uint32_t unit = tid / kBC + i * (64u * kW / kBC);
-      raw[i] = *reinterpret_cast<const u32x2v*>(q + mx_at<kRawRow>(raw_row, unit >> 1) + (unit & 1u) * 8u);
-      raw_s[i] = mx_scale(q[kRawBytes + raw_row * (kBN / 32u) + unit * kPer / 4u]);
-    }
-    if ((step + 1u) * kBC > c1) {  // zeros behind the contraction's end
-#pragma unroll
-      for (uint32_t i = 0; i < kUnits; i++)
-        if (step * kBC + raw_row >= c1) {
-          raw[i] = u32x2v{0u, 0u};
-          raw_s[i] = 1.0f;
-        }
-    }
-  };
-  const auto raw_write = [&](uint32_t part, uint8_t* tile) {  // part of kSub
-    constexpr uint32_t kPieces = kUnits * kPer;
-#pragma unroll
-    for (uint32_t piece = 0; piece < kPieces; piece++) {
-      if (piece * kSub / kPieces != part) continue;
-      const uint32_t i = piece / kPer, h = piece % kPer;
-      const uint32_t unit = tid / kBC + i * (64u * kW / kBC);
-      const uint32_t at = raw_row * (kBN * 2u) + (((unit * kPer + h) ^ mx_turn_cols(raw_row)) << 4);
-      *reinterpret_cast<u32x4v*>(tile + at) =
-          kOp == kMxWgrad ? mx_unit8(raw[i][0], raw[i][1], raw_s[i]) : mx_unit4(raw[i][h], raw_s[i]);
+      b_next += uint64_t(kBC) * b_pitch;
+      bs_next += uint64_t(kBC) * s_pitch;
     }
   };
 
   // A wave's row fragments lie kWM apart, so that where the group's rows end
   // inside the tile every wave has as few left (matmul, dx).
+  typedef __attribute__((address_space(3))) v2i lds_v2i;
+  typedef __attribute__((address_space(3))) v4s lds_v4s;
   const uint32_t wm = (wave / kWN) * 32u, wn = (wave % kWN) * (kBN / kWN);
   constexpr uint32_t kMStep = kWM * 32u;
   v16f acc[kFM][kFN];
@@ -729,16 +761,14 @@ __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_
 #pragma unroll
       for (int r = 0; r < 16; r++) acc[i][j][r] = 0.0f;
 
-  // Batch b of loads: A of step b and the mx operand of step b (matmul) or
-  // b + 1, whose BF16 tile is made during step b.  kStages - 1 batches are in
+  // Batch b of loads: both operands of step b.  kStages - 1 batches are in
   // flight while a step computes.
   const auto next_slot = [](uint32_t s) { return s + 1u == kStages ? 0u : s + 1u; };
   const auto batch = [&](uint32_t b, uint32_t slot) {
     if constexpr (kRowsB)
       if (b % 8u == 0u) load_scales(b / 8u);
     load_a(b, slot);
-    if constexpr (kRowsB) load_b(b, slot);
-    else load_b(min(b + 1u, steps - 1u), next_slot(slot));
+    load_b(b, slot);
   };
   // All but the last kBatches batches have landed.  Every wave counts its own
   // loads: those that fetch scale words have one more in each batch (in a
@@ -748,19 +778,9 @@ __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_
     if (!kRowsB && wave * 64u < kScaleWords) mx_fence<kBatches * int(kDma + 1u)>();
     else mx_fence<kBatches * int(kDma)>();
   };
-  if (steps) {
-    if constexpr (!kRowsB) load_b(0u, 0u);
 #pragma unroll
-    for (uint32_t b = 0; b + 1u < kStages; b++)
-      if (b < steps) batch(b, b);
-    if constexpr (!kRowsB) {
-      if (steps + 1u >= kStages) fence(std::integral_constant<int, int(kStages) - 1>());
-      else mx_fence<0>();
-      raw_read(0u, 0u);
-#pragma unroll
-      for (uint32_t q = 0; q < kSub; q++) raw_write(q, lds + kStages * kStage);
-    }
-  }
+  for (uint32_t b = 0; b + 1u < kStages; b++)
+    if (b < steps) batch(b, b);
   int left_b[kFN], left_a[kFM];
   if constexpr (kRowsB) {
 #pragma unroll
@@ -818,40 +838,60 @@ __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_
             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
       }
     } else {
-      const uint8_t* tile = lds + kStages * kStage + (step & 1u) * kTile;
-      uint8_t* next = lds + kStages * kStage + ((step + 1u) & 1u) * kTile;
-      if (step + 1u < steps) raw_read(step + 1u, next_slot(slot));
-      v8bf fa[2][kFM], fb[2][kFN];
-      const auto frags = [&](uint32_t s, v8bf* to_a, v8bf* to_b) {
-        // this lane's contraction row of a transposing read, and its turn
-        const uint32_t c = s * 16u + half * 8u + ((lane >> 2) & 3u);
-        const uint32_t t0 = mx_turn_cols(c) << 4, t1 = mx_turn_cols(c + 4u) << 4;
-        const uint32_t piece = ((lane >> 4) & 1u) * 32u + (lane & 3u) * 8u;
+      uint8_t* sb = lds + slot * kStage + kABytes;
+      if ((step + 1u) * kBC > c1) {  // the last step: zeros behind the contraction's end
+        const uint32_t have = c1 - step * kBC;
+        for (uint32_t i = have * kRawPer + tid; i < kBC * kRawPer; i += 64u * kW)
+          *reinterpret_cast<u32x4v*>(sb + i * 16u) = u32x4v{0u, 0u, 0u, 0u};
+        for (uint32_t i = tid; i < kScaleWords; i += 64u * kW)
+          if (i % kBC >= have) *reinterpret_cast<uint32_t*>(sb + kRawBytes + i * 4u) = 0x7F7F7F7Fu;
+        mx_fence<0>();
+      }
+#pragma unroll
+      for (uint32_t s = 0; s < kSub; s++) {
+        const uint32_t c = s * 16u + half * 8u;  // this lane half's eight contraction rows
+        const uint8_t* ss = sb + kRawBytes + (wn / 128u * kBC + c) * 4u;
+        const u32x4v w0 = *reinterpret_cast<const u32x4v*>(ss), w1 = *reinterpret_cast<const u32x4v*>(ss + 16);
+        v8bf fa[kFM], fb[kFN];
+        const uint32_t ct = c + ((lane >> 2) & 3u);  // this lane's row where four are gathered
 #pragma unroll
         for (uint32_t i = 0; i < kFM; i++) {
           if constexpr (kOp == kMxWgrad) {
-            const uint32_t byte = (wm + i * kMStep) * 2u + piece;
-            to_a[i] = mx_read_cols(sa + c * kARow + (byte ^ t0), sa + (c + 4u) * kARow + (byte ^ t1));
+            const uint32_t byte = (wm + i * kMStep) * 2u + ((lane >> 4) & 1u) * 32u + (lane & 3u) * 8u;
+            fa[i] = mx_read_cols(sa + ct * kARow + (byte ^ (mx_turn_cols(ct) << 4)),
+                                 sa + (ct + 4u) * kARow + (byte ^ (mx_turn_cols(ct + 4u) << 4)));
           } else {
-            to_a[i] = *reinterpret_cast<const v8bf*>(sa + mx_at<kARow>(wm + i * kMStep + (lane & 31u), s * 2u + half));
+            fa[i] = *reinterpret_cast<const v8bf*>(sa + mx_at<kARow>(wm + i * kMStep + (lane & 31u), s * 2u + half));
           }
         }
 #pragma unroll
-        for (uint32_t j = 0; j < kFN; j++) {
-          const uint32_t byte = (wn + j * 32u) * 2u + piece;
-          to_b[j] = mx_read_cols(tile + c * (kBN * 2u) + (byte ^ t0), tile + (c + 4u) * (kBN * 2u) + (byte ^ t1));
+        for (uint32_t j = 0; j < kFN; j += 2u) {
+          const uint32_t block = wn / 32u + j + ((lane >> 4) & 1u);  // of this lane's columns
+          uint32_t q[kBBits / 2u];
+          if constexpr (kOp == kMxWgrad) {
+            const uint32_t byte = block * 32u + (lane & 3u) * 8u;
+            const uint8_t* at = sb + ct * kRawRow + (byte ^ (mx_turn_pairs<8, kRawRow>(ct) << 4));
+            const v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)at);
+            const v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(at + 4u * kRawRow));
+            const u32x2v l = __builtin_bit_cast(u32x2v, lo), h = __builtin_bit_cast(u32x2v, hi);
+            q[0] = l[0];
+            q[1] = l[1];
+            q[2] = h[0];
+            q[3] = h[1];
+          } else {
+            const uint32_t r = c + ((lane >> 1) & 7u);
+            const v2i v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                (lds_v2i*)(sb + r * kRawRow + ((block ^ mx_turn_pairs<4, kRawRow>(r)) << 4) + (lane & 1u) * 8u));
+            q[0] = uint32_t(v[0]);
+            q[1] = uint32_t(v[1]);
+          }
+          mx_pairs<int(kBBits)>(q, w0, w1, (block & 3u) * 8u + 9u, fb[j], fb[j + 1u]);
         }
-      };
-      frags(0u, fa[0], fb[0]);
-#pragma unroll
-      for (uint32_t s = 0; s < kSub; s++) {
-        if (s + 1u < kSub) frags(s + 1u, fa[(s + 1u) & 1u], fb[(s + 1u) & 1u]);
 #pragma unroll
         for (uint32_t i = 0; i < kFM; i++)
 #pragma unroll
           for (uint32_t j = 0; j < kFN; j++)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[s & 1u][j], fa[s & 1u][i], acc[i][j], 0, 0, 0);
-        if (step + 1u < steps) raw_write(s, next);
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
       }
     }
     slot = next_slot(slot);
@@ -861,8 +901,13 @@ __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_
   for (uint32_t i = 0; i < kFM; i++) {
     const uint32_t row = m0 + wm + i * kMStep + (lane & 31u);
     const uint64_t at = kOp == kMxWgrad ? ((uint64_t(part) * p.groups + g) * p.n + row) * p.k : uint64_t(row) * p.ldo;
+    if constexpr (kRowsB) {
 #pragma unroll
-    for (uint32_t j = 0; j < kFN; j++) mx_store_frag(p, row < m1, at, n0 + wn + j * 32u, cols, acc[i][j]);
+      for (uint32_t j = 0; j < kFN; j++) mx_store_frag(p, row < m1, at, n0 + wn + j * 32u, cols, acc[i][j]);
+    } else if (row < m1) {
+#pragma unroll
+      for (uint32_t j = 0; j < kFN; j += 2u) mx_store_pair(p, at, n0 + wn + j * 32u, cols, acc[i][j], acc[i][j + 1u]);
+    }
   }
 }
 
@@ -1347,11 +1392,10 @@ template <int kOp>
 ciera_status mx_gemm(const MxArgs& p, hipStream_t stream) {
   if constexpr (kOp == kMxDx) {
     const uint64_t tiles = mx_tiles(p, p.k);
-    if (mx_rows_each(p) >= 1024u && tiles >= 2u * kMxCus) return mx_gemm_as<kOp, 256u, 256u, 64u, 2u, 4u, 2u, 1u>(p, stream);
     if (mx_rows_each(p) > 96u && mx_token_tiles(p, 64u) * cdiv(p.k, 256u) > 2u * kMxCus)
-      return mx_gemm_as<kOp, 128u, 256u, 32u, 2u, 2u, 3u, 2u>(p, stream);
-    if (mx_token_tiles(p, 64u) * cdiv(p.k, 128u) <= 2u * kMxCus) return mx_gemm_as<kOp, 64u, 128u, 64u, 1u, 4u, 3u, 2u>(p, stream);
-    return mx_gemm_as<kOp, 64u, 256u, 32u, 1u, 4u, 4u, 2u>(p, stream);
+      return mx_gemm_as<kOp, 128u, 256u, 64u, 1u, 4u, 3u, 2u>(p, stream);
+    if (mx_token_tiles(p, 64u) * cdiv(p.k, 128u) <= 2u * kMxCus) return mx_gemm_as<kOp, 64u, 128u, 64u, 2u, 2u, 3u, 2u>(p, stream);
+    return mx_gemm_as<kOp, 64u, 256u, 64u, 1u, 4u, 2u, 3u>(p, stream);
   } else {
     const uint64_t tiles = mx_tiles(p, p.n);
     if (mx_rows_each(p) > 64u && tiles >= 2u * kMxCus) return mx_gemm_as<kOp, 128u, 256u, 64u, 2u, 2u, 3u, 2u>(p, stream);
