@@ -233,7 +233,7 @@ struct MxArgs {
   Ctrl* ctrl;
   uint32_t* status;
   uint32_t tokens, n, k, kp, groups;
-  uint32_t parts;  // wgrad: the contraction in this many parts, each with an output of its own
+  uint32_t parts;  // dx, wgrad: the contraction in this many parts, each with an output of its own
   uint32_t out_f32, accumulate;
 };
 
@@ -584,7 +584,7 @@ __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_
   uint32_t g, m0, m1, n0, c1;
   const uint32_t cols = kRowsB ? p.n : p.k;
   const uint32_t ntiles = (cols + kBN - 1u) / kBN;
-  uint32_t r0 = 0u, part = 0u;  // first contraction row, and which part of them (wgrad)
+  uint32_t r0 = 0u, part = 0u;  // first contraction row, and which part of them (wgrad; dx: of n)
   if constexpr (kOp == kMxWgrad) {
     const uint32_t mtiles = (p.n + kBM - 1u) / kBM;
     const uint32_t at = mx_xcd_run(blockIdx.x, gridDim.x);
@@ -609,6 +609,12 @@ __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_
     m1 = t.row1;
     n0 = t.col * kBN;
     c1 = kRowsB ? p.k : p.n;
+    if constexpr (kOp == kMxDx) {
+      part = blockIdx.y;
+      const uint32_t each = (c1 + p.parts * kBC - 1u) / (p.parts * kBC) * kBC;
+      r0 = min(part * each, c1);
+      c1 = min(each, c1 - r0);
+    }
   }
   const uint32_t steps = (c1 + kBC - 1u) / kBC;
   const uint32_t lds0 = mx_lds(lds);
@@ -634,7 +640,7 @@ __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_
     }
   } else {
     const uint64_t pitch = kOp == kMxMatmul8 ? p.kp : p.lda * 2u;
-    a_next = (kOp == kMxMatmul8 ? p.xq : reinterpret_cast<const uint8_t*>(p.a)) + uint64_t(m0) * pitch;
+    a_next = (kOp == kMxMatmul8 ? p.xq : reinterpret_cast<const uint8_t*>(p.a + r0)) + uint64_t(m0) * pitch;
 #pragma unroll
     for (uint32_t i = 0; i < kDmaA; i++) {
       const uint32_t pos = (i * kW + wave) % kALoads * 64u + lane, r = pos / kAPer;
@@ -655,7 +661,7 @@ __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_
       } else {
         const uint32_t c = c0 + ((pos % kAPer) ^ mx_turn<kARow>(r)) * 8u;
         have = c < c1 ? c1 - c : 0u;
-        at = (uint64_t(m0) + min(r, m1 - 1u - m0)) * p.lda + c;
+        at = (uint64_t(m0) + min(r, m1 - 1u - m0)) * p.lda + r0 + c;
       }
       const uint16_t* src = p.a + (have ? at : 0u);
       *reinterpret_cast<u32x4v*>(to + pos * 16u) =
@@ -680,7 +686,7 @@ __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_
   uint32_t b_off[kDmaRaw], b_row[kDmaRaw], bs_off = 0u, bs_row = 0u;
   const uint32_t b_pitch = p.kp * kBBits / 8u, s_pitch = p.kp / 32u;
   {
-    const uint64_t row = kOp == kMxWgrad ? uint64_t(r0) : uint64_t(g) * p.n + (kRowsB ? n0 : 0u);
+    const uint64_t row = kOp == kMxWgrad ? uint64_t(r0) : uint64_t(g) * p.n + (kRowsB ? n0 : r0);
     b_next = (kOp == kMxWgrad ? p.xq : p.wq) + row * b_pitch;
     bs_next = (kOp == kMxWgrad ? p.xs : p.ws) + row * s_pitch;
 #pragma unroll
@@ -900,7 +906,8 @@ __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_
 #pragma unroll
   for (uint32_t i = 0; i < kFM; i++) {
     const uint32_t row = m0 + wm + i * kMStep + (lane & 31u);
-    const uint64_t at = kOp == kMxWgrad ? ((uint64_t(part) * p.groups + g) * p.n + row) * p.k : uint64_t(row) * p.ldo;
+    const uint64_t at = kOp == kMxWgrad ? ((uint64_t(part) * p.groups + g) * p.n + row) * p.k
+                                         : (uint64_t(part) * p.tokens + row) * p.ldo;
     if constexpr (kRowsB) {
 #pragma unroll
       for (uint32_t j = 0; j < kFN; j++) mx_store_frag(p, row < m1, at, n0 + wn + j * 32u, cols, acc[i][j]);
@@ -1255,6 +1262,32 @@ __global__ __launch_bounds__(kMxThreads) void k_mx_join(MxArgs p, const float* _
   }
 }
 
+// dx's, for one row of a group; other rows are left as they are.
+__global__ __launch_bounds__(kMxThreads) void k_mx_join_rows(MxArgs p, const float* __restrict__ sums) {
+  const uint32_t row = blockIdx.x;
+  bool live = !p.offsets;
+  for (uint32_t g = threadIdx.x & 63u; g < p.groups && !live; g += 64u) {
+    uint32_t r0, r1;
+    mx_rows(p, g, r0, r1);
+    live = row >= r0 && row < r1;
+  }
+  if (!__any(live)) return;
+  const uint64_t count = uint64_t(p.tokens) * p.k, from = uint64_t(row) * p.k, to = uint64_t(row) * p.ldo;
+  for (uint32_t c = threadIdx.x * 4u; c < p.k; c += kMxThreads * 4u) {
+    if (c + 4u <= p.k) {
+      v4f v = *reinterpret_cast<const v4fa4*>(sums + from + c);
+      for (uint32_t i = 1; i < p.parts; i++) v += v4f(*reinterpret_cast<const v4fa4*>(sums + i * count + from + c));
+      mx_store4(p, to + c, v);
+    } else {
+      for (uint32_t j = c; j < p.k; j++) {
+        float v = sums[from + j];
+        for (uint32_t i = 1; i < p.parts; i++) v += sums[i * count + from + j];
+        mx_store(p, to + j, v);
+      }
+    }
+  }
+}
+
 ciera_status mx_matrix(const void* d_m, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t align) {
   if (rows > kMxMaxRows || cols > kMxMaxCols || ld < cols || ld > kMxMaxLd) return CIERA_ERR_ARG;
   if (rows && cols && (!d_m || (reinterpret_cast<uintptr_t>(d_m) & (align - 1u)) != 0u)) return CIERA_ERR_ARG;
@@ -1303,13 +1336,15 @@ ciera_status mx_decode_impl(const void* d_q, uint64_t q_bytes, uint64_t rows, ui
 
 constexpr uint32_t kMxCus = 256u;
 uint32_t mx_wgrad_parts(uint64_t tokens, uint64_t n, uint64_t k, uint64_t groups);
+uint32_t mx_dx_parts(uint64_t tokens, uint64_t n, uint64_t k, uint64_t groups);
 
 uint64_t mx_ws_size(uint64_t tokens, uint64_t n, uint64_t k, uint64_t groups) {
   if (tokens > kMxMaxRows - 1u || !n || !k || n > kMxMaxCols || k > kMxMaxCols || !groups || groups > kMxMaxGroups ||
       groups * n > kMxMaxRows)
     return 0u;
-  const uint64_t parts = mx_wgrad_parts(tokens, n, k, groups);
-  return kMxWsHead + (parts > 1u ? parts * groups * n * k * 4u : 0u);
+  const uint64_t wgrad = mx_wgrad_parts(tokens, n, k, groups), dx = mx_dx_parts(tokens, n, k, groups);
+  const uint64_t sums = wgrad > 1u ? wgrad * groups * n * k : 0u, rows = dx > 1u ? dx * tokens * k : 0u;
+  return kMxWsHead + (sums > rows ? sums : rows) * 4u;
 }
 
 // The checks every product makes, and the arguments they share.
@@ -1348,9 +1383,11 @@ ciera_status mx_product(MxArgs& p, const void* d_w, uint64_t w_bytes, void* d_ou
 }
 
 // Token tiles of bm rows that the groups can need between them.
+uint64_t mx_token_tiles(uint64_t tokens, uint64_t groups, uint32_t bm) {
+  return tokens / bm + (groups < tokens ? groups : tokens);
+}
 uint64_t mx_token_tiles(const MxArgs& p, uint32_t bm) {
-  if (!p.offsets) return cdiv(p.tokens, bm);
-  return p.tokens / bm + (p.groups < p.tokens ? p.groups : p.tokens);
+  return p.offsets ? mx_token_tiles(p.tokens, p.groups, bm) : cdiv(p.tokens, bm);
 }
 
 // What the rules below go by: tiles of 128 x 256 that the output would make,
@@ -1364,7 +1401,7 @@ ciera_status mx_gemm_as(const MxArgs& p, hipStream_t stream) {
   const uint64_t mtiles = kOp == kMxWgrad ? cdiv(p.n, kBM) * p.groups * p.parts : mx_token_tiles(p, kBM);
   const uint64_t grid = mtiles * cdiv(kRowsB ? p.n : p.k, kBN);
   if (grid > 0x7FFFFFFFu) return CIERA_ERR_ARG;
-  launch(k_mx_gemm<kOp, kBM, kBN, kBC, kWM, kWN, kStages, kPerCu>, dim3(uint32_t(grid)), dim3(kWM * kWN * 64u), stream, p);
+  launch(k_mx_gemm<kOp, kBM, kBN, kBC, kWM, kWN, kStages, kPerCu>, dim3(uint32_t(grid), kOp == kMxDx ? p.parts : 1u), dim3(kWM * kWN * 64u), stream, p);
   return launch_status();
 }
 template <uint32_t kBM, uint32_t kBN, uint32_t kWM, uint32_t kWN, uint32_t kStages, uint32_t kPerCu>
@@ -1443,6 +1480,31 @@ uint32_t mx_wgrad_parts(uint64_t tokens, uint64_t n, uint64_t k, uint64_t groups
   uint64_t parts = 2u * kMxCus / tiles;
   if (parts > tokens / groups / 512u) parts = tokens / groups / 512u;
   return parts < 1u ? 1u : parts > 8u ? 8u : uint32_t(parts);
+}
+// dx: where even its smallest tiles leave CUs without a workgroup, n goes in up
+// to eight parts of at least 256, joined likewise.
+uint32_t mx_dx_parts(uint64_t tokens, uint64_t n, uint64_t k, uint64_t groups) {
+  const uint64_t tiles = mx_token_tiles(tokens, groups, 64u) * cdiv(k, 128u);
+  uint64_t parts = tiles ? kMxCus / tiles : 1u;
+  if (parts > n / 256u) parts = n / 256u;
+  return parts < 1u ? 1u : parts > 8u ? 8u : uint32_t(parts);
+}
+ciera_status mx_dx_impl(MxArgs p, hipStream_t stream) {
+  (void)hipGetLastError();
+  if (p.tokens == 0u) {
+    launch(k_mx_status, dim3(1), dim3(64), stream, p);
+    return launch_status();
+  }
+  p.parts = mx_dx_parts(p.tokens, p.n, p.k, p.groups);
+  if (p.parts == 1u) return mx_gemm<kMxDx>(p, stream);
+  MxArgs sums = p;
+  sums.out = reinterpret_cast<uint8_t*>(p.ctrl) + kMxWsHead;
+  sums.ldo = p.k;
+  sums.out_f32 = 1u;
+  const ciera_status st = mx_gemm<kMxDx>(sums, stream);
+  if (st != CIERA_OK) return st;
+  launch(k_mx_join_rows, dim3(p.tokens), dim3(kMxThreads), stream, p, static_cast<const float*>(sums.out));
+  return launch_status();
 }
 ciera_status mx_wgrad_impl(MxArgs p, hipStream_t stream) {
   (void)hipGetLastError();
@@ -1524,12 +1586,7 @@ ciera_status mx4_matmul_dx(const void* d_dy, uint64_t lddy, const void* d_w, uin
   if (st != CIERA_OK) return st;
   p.a = static_cast<const uint16_t*>(d_dy);
   p.lda = lddy;
-  (void)hipGetLastError();
-  if (p.tokens == 0u) {
-    launch(k_mx_status, dim3(1), dim3(64), stream, p);
-    return launch_status();
-  }
-  return mx_gemm<kMxDx>(p, stream);
+  return mx_dx_impl(p, stream);
 }
 
 ciera_status mx8_wgrad(const void* d_dy, uint64_t lddy, const void* d_xq, uint64_t xq_bytes, void* d_dw,
