@@ -544,11 +544,20 @@ __device__ __forceinline__ v8bf mx_read_cols(const uint8_t* at0, const uint8_t* 
 //           matrix instructions, a quarter of the LDS traffic of a BF16 tile.
 //           Lane half h so holds values 32 h .. 32 h + 31 of the step, eight
 //           per instruction; x is read in the same order.  x in mx8 likewise.
-//   dx      M tokens, N k, contraction n: W's rows are contraction rows; its
-//           scales differ along them, so it becomes BF16 on the way to a
-//           second LDS tile (one step ahead) that is read back transposed.
-//   wgrad   M n, N k, contraction the group's tokens: the same for x, and dy
-//           is read back transposed too.
+//   dx      M tokens, N k, contraction n: W's rows are contraction rows, so it
+//           is read transposed, in 4 bits; its scales differ from row to row,
+//           and a lane converts two neighbouring columns of a row together
+//           (mx_pairs: 1.5 instructions a value).  dy is read like x.
+//   wgrad   M n, N k, contraction the group's tokens: the same for x in 8
+//           bits, and dy is read transposed too.
+// A BF16 copy of the tile in LDS, made a step ahead, was slower (dx of 4,000
+// rows in 64 groups: 52 against 32 us): 16-byte LDS writes reach 65 B a clock.
+// What bounds them: the matrix instructions' 1.83 PFLOP/s at the clock that
+// their power leaves, then what a tile cannot hide (dx of 32,768 rows in one
+// group, n = k = 2,048: 258 us, 1.07 PFLOP/s; without its loads 25, conversions
+// 28, stores 20 us less).  Measured at n = 1,024, k = 2,048, 64 groups of 512
+// rows on average: dx 167 us, wgrad 220 us (268 MB of results, no tile shape
+// within 5 % of it faster); matmul of 4,001 x 2,048 x 2,048: 34 us.
 template <int kOp, uint32_t kBM, uint32_t kBN, uint32_t kBC, uint32_t kWM, uint32_t kWN, uint32_t kStages, uint32_t kPerCu>
 __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_gemm(MxArgs p) {
   constexpr bool kRowsB = kOp == kMxMatmul || kOp == kMxMatmul8;  // B runs along the contraction
@@ -1422,14 +1431,12 @@ ciera_status mx_gemm8_as(const MxArgs& p, hipStream_t stream) {
 //           128 rows, 128 or 256 columns: 4,001: 37, 41; 8,192: 72, 69; 32,768: 265, 252.
 //           x in mx8, BF16 result (the scaled instructions), 32 or 64 rows: 2,048: 21, 16; 2,000 in 64 g: 17.5, 23;
 //           6,000 in 64 g: 32, 29; 64 or 128 rows: 3,000: 24, 24; 8,192: 56, 44; 6,000 in 64 g: 29, 34.
-//   dx      64 x 128 or 64 x 256: 40: 25, 42; 1,024 in 8 g: 19, 25; 1,000 in 64 g: 36, 31; 4,000 in 64 g: 53, 51.
-//           64 or 128 rows: 8,192 in 64 g: 78, 66; 32,768 in 64 g: 242, 187.
-//           128 or 256 rows: 8,192: 85, 76; 32,768: 296, 273; 16,384 in 32 g: 103, 103; 65,536 in 32 g: 332, 317.
+//   dx      64 x 128 or 64 x 256: 512: 23, 29; 2,048: 34, 33; 64 in 64 g: 27, 22; 4,000 in 64 g: 40, 32.
+//           64 or 128 rows: 4,096: 49, 47; 8,192: 79, 73; 32,768: 277, 258; 8,192 in 8 g: 50, 52; 32,768 in 64 g: 167, 170.
 template <int kOp>
 ciera_status mx_gemm(const MxArgs& p, hipStream_t stream) {
   if constexpr (kOp == kMxDx) {
-    const uint64_t tiles = mx_tiles(p, p.k);
-    if (mx_rows_each(p) > 96u && mx_token_tiles(p, 64u) * cdiv(p.k, 256u) > 2u * kMxCus)
+    if (mx_rows_each(p) >= 1024u && mx_tiles(p, p.k) >= 2u * kMxCus)
       return mx_gemm_as<kOp, 128u, 256u, 64u, 1u, 4u, 3u, 2u>(p, stream);
     if (mx_token_tiles(p, 64u) * cdiv(p.k, 128u) <= 2u * kMxCus) return mx_gemm_as<kOp, 64u, 128u, 64u, 2u, 2u, 3u, 2u>(p, stream);
     return mx_gemm_as<kOp, 64u, 256u, 64u, 1u, 4u, 2u, 3u>(p, stream);
@@ -1472,8 +1479,8 @@ ciera_status mx_matmul_impl(MxArgs& p, hipStream_t stream) {
 
 // wgrad: where the tiles would leave CUs idle, each group's tokens go in up to
 // eight parts, at least 512 rows each on average, whose FP32 sums k_mx_join
-// adds in order (n = k = 2,048, FP32: 8,192 rows 100 against 185 us in one
-// part, 2,048 rows 47 against 55; 1,024 rows in parts of 256: 38 against 33 in
+// adds in order (n = k = 2,048, FP32: 8,192 rows 95 against 174 us in one
+// part, 2,048 rows 43 against 52; 1,024 rows in parts of 256: 36 against 30 in
 // one).
 uint32_t mx_wgrad_parts(uint64_t tokens, uint64_t n, uint64_t k, uint64_t groups) {
   const uint64_t tiles = cdiv(n, 256u) * cdiv(k, 128u) * groups;
@@ -1482,7 +1489,8 @@ uint32_t mx_wgrad_parts(uint64_t tokens, uint64_t n, uint64_t k, uint64_t groups
   return parts < 1u ? 1u : parts > 8u ? 8u : uint32_t(parts);
 }
 // dx: where even its smallest tiles leave CUs without a workgroup, n goes in up
-// to eight parts of at least 256, joined likewise.
+// to eight parts of at least 256, joined likewise (n = k = 2,048: 40 rows 14.5
+// against 23.0 us in one part, 256 rows 16.2 against 23.3).
 uint32_t mx_dx_parts(uint64_t tokens, uint64_t n, uint64_t k, uint64_t groups) {
   const uint64_t tiles = mx_token_tiles(tokens, groups, 64u) * cdiv(k, 128u);
   uint64_t parts = tiles ? kMxCus / tiles : 1u;
