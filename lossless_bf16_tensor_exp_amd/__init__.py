@@ -1,9 +1,10 @@
 """Lossless BF16 codec for MI355X: exponent reuse across iterations (CIERA)
-plus the sigma-windowed 3-bit exponent code (ZipCCL), in hand-written HIP.
+plus the sigma-windowed 3-bit exponent code (ZipCCL), in hand-written HIP; and
+matrices in 8 and 4 bits with the products of a linear layer on them.
 
 This package is a thin binding over the C ABI in ``include/ciera.h``
 (``libciera.so``, built in-tree by ``build.py``).  Every step of the codec
-runs in the HIP kernels; the binding only checks tensor types and passes
+and of the products runs in the HIP kernels; the binding only checks tensor types and passes
 device pointers, sizes and the current HIP stream.  PyTorch supplies device
 memory and streams and nothing else.  If the library is not built, every
 entry point raises: there is no fallback.

@@ -1,8 +1,8 @@
 """Compile the HIP library in-tree: ``lossless_bf16_tensor_exp_amd/libciera.so``.
 
 One hipcc call for gfx950.  Packed FP32 instructions are switched off and
-FP32 denormals kept, so the only floating-point work (the FP64 variance
-sums) runs on plain scalar instructions.
+FP32 denormals kept, so the codec's only floating-point work (the FP64
+variance sums) runs on plain scalar instructions.
 """
 from __future__ import annotations
 
