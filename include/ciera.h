@@ -454,8 +454,8 @@ ciera_status ciera_encode_ex(const void* d_x, uint64_t n, uint32_t B, uint8_t* d
  * matrix is empty). */
 uint64_t mx8_encoded_size(uint64_t rows, uint64_t cols);
 uint64_t mx4_encoded_size(uint64_t rows, uint64_t cols);
-/* Workspace bytes of the four products (one size serves all of them); 0 when
- * a size is out of range. */
+/* Workspace bytes of the four products (one size serves all of them, and every
+ * smaller number of tokens); 0 when a size is out of range. */
 uint64_t mx_workspace_size(uint64_t tokens, uint64_t n, uint64_t k, uint32_t groups);
 
 /* mx8_encode, mx4_encode:  d_x  in, rows x cols BF16, row stride ld;  d_q  out,

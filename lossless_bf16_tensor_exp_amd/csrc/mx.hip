@@ -1344,16 +1344,21 @@ ciera_status mx_decode_impl(const void* d_q, uint64_t q_bytes, uint64_t rows, ui
 }
 
 constexpr uint32_t kMxCus = 256u;
+constexpr uint32_t kMxDxParts = 8u;
 uint32_t mx_wgrad_parts(uint64_t tokens, uint64_t n, uint64_t k, uint64_t groups);
-uint32_t mx_dx_parts(uint64_t tokens, uint64_t n, uint64_t k, uint64_t groups);
 
 uint64_t mx_ws_size(uint64_t tokens, uint64_t n, uint64_t k, uint64_t groups) {
   if (tokens > kMxMaxRows - 1u || !n || !k || n > kMxMaxCols || k > kMxMaxCols || !groups || groups > kMxMaxGroups ||
       groups * n > kMxMaxRows)
     return 0u;
-  const uint64_t wgrad = mx_wgrad_parts(tokens, n, k, groups), dx = mx_dx_parts(tokens, n, k, groups);
-  const uint64_t sums = wgrad > 1u ? wgrad * groups * n * k : 0u, rows = dx > 1u ? dx * tokens * k : 0u;
-  return kMxWsHead + (sums > rows ? sums : rows) * 4u;
+  // Sized for every smaller number of tokens too, some of which dx takes in
+  // more parts: as parts * tiles <= kMxCus and tokens < 64 tiles / columns'
+  // tiles, the parts' rows stay below 64 kMxCus / columns' tiles.
+  const uint64_t wgrad = mx_wgrad_parts(tokens, n, k, groups), cols = cdiv(k, 128u);
+  const uint64_t sums = wgrad > 1u ? wgrad * groups * n * k : 0u;
+  uint64_t rows = n >= 512u && cols <= kMxCus / 2u ? 64u * kMxCus / cols : 0u;
+  if (rows > kMxDxParts * tokens) rows = kMxDxParts * tokens;
+  return kMxWsHead + (sums > rows * k ? sums : rows * k) * 4u;
 }
 
 // The checks every product makes, and the arguments they share.
@@ -1495,7 +1500,7 @@ uint32_t mx_dx_parts(uint64_t tokens, uint64_t n, uint64_t k, uint64_t groups) {
   const uint64_t tiles = mx_token_tiles(tokens, groups, 64u) * cdiv(k, 128u);
   uint64_t parts = tiles ? kMxCus / tiles : 1u;
   if (parts > n / 256u) parts = n / 256u;
-  return parts < 1u ? 1u : parts > 8u ? 8u : uint32_t(parts);
+  return parts < 1u ? 1u : parts > kMxDxParts ? kMxDxParts : uint32_t(parts);
 }
 ciera_status mx_dx_impl(MxArgs p, hipStream_t stream) {
   (void)hipGetLastError();

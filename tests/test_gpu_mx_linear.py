@@ -94,6 +94,32 @@ def test_step_and_gradient_exchange(tokens, n, k, groups, tail):
 
 
 @pytest.mark.gpu
+def test_fewer_rows_than_the_layer_was_made_for():
+    """Few rows go through other kernels and parts than many; one layer's workspace serves all."""
+    require_gpu()
+    from lossless_bf16_tensor_exp_amd.codec import MxLinear
+    n, k = 4096, 4224
+    gen = torch.Generator().manual_seed(9)
+    w = torch.tensor([0.0, 1, -1, 2, -2, 3, 6])[torch.randint(0, 7, (n, k), generator=gen)]
+    w[:, ::32] = 6.0
+    layer = MxLinear(700, n, k)
+    layer.load(w.to(torch.bfloat16).cuda())
+    for tokens in (1, 40, 130, 700, 3):
+        say(f"layer of 700 with {tokens} rows")
+        x, dy = (torch.randint(-8, 9, (tokens, c), generator=gen).to(torch.bfloat16) for c in (k, n))
+        y = torch.zeros(tokens, n, device="cuda")
+        dx = torch.zeros(tokens, k, device="cuda")
+        dw = torch.zeros(n, k, device="cuda")
+        layer.keep(x.cuda(), y)
+        layer.backward(dy.cuda(), dx, dw)
+        assert layer.error() == 0
+        # whole numbers below 2^24: FP32 holds every partial sum exactly
+        assert torch.equal(y.cpu(), x.float() @ w.t())
+        assert torch.equal(dx.cpu(), dy.float() @ w)
+        assert torch.equal(dw.cpu(), dy.float().t() @ x.float())
+
+
+@pytest.mark.gpu
 def test_captured_step_takes_new_weights_and_rows():
     """keep and backward in one graph: each replay sees what the buffers hold then, the offsets included."""
     require_gpu()
