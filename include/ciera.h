@@ -430,7 +430,9 @@ ciera_status ciera_encode_ex(const void* d_x, uint64_t n, uint32_t B, uint8_t* d
  * Sizes: rows <= 2^31; cols, n, k <= 2^21; groups <= 4096; groups * n <= 2^31;
  * row strides (ld*, in values) from the number of columns to 2^22.  BF16 and
  * FP32 matrices need the alignment of their type only, and rows may start
- * anywhere; encoded matrices and the workspace are 16-byte aligned.
+ * anywhere; encoded matrices and the workspace are 16-byte aligned.  A call
+ * that would need 2^32 threads (matrices of 2^36 values and more) is
+ * CIERA_ERR_ARG.
  *
  * Groups: the products take `groups` weight matrices of n x k at once, encoded
  * as one matrix of groups * n rows.  Rows d_offsets[g] .. d_offsets[g + 1] - 1

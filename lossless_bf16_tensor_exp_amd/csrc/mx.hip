@@ -38,6 +38,7 @@ constexpr uint64_t kMxMaxRows = 1ull << 31;
 constexpr uint64_t kMxMaxCols = 1ull << 21;
 constexpr uint64_t kMxMaxLd = 1ull << 22;
 constexpr uint32_t kMxMaxGroups = 4096u;
+constexpr uint64_t kMxMostThreads = 0xFFFFFFFFu;  // of a launch
 constexpr uint64_t kMxWsHead = 512u;  // control block, then the one status word
 
 __host__ __device__ constexpr uint64_t mx_pitch(uint64_t cols) { return (cols + 127u) & ~uint64_t(127); }
@@ -502,7 +503,8 @@ __device__ __forceinline__ uint32_t mx_lds(const void* at) {
 // choosing which chunk a lane fetches.
 template <uint32_t kRow>
 __device__ __forceinline__ uint32_t mx_turn(uint32_t r) {
-  return kRow >= 256u ? (r & 15u) : (r / (256u / kRow)) & (kRow / 16u - 1u);
+  static_assert(kRow == 64u || kRow == 128u, "4 or 8 chunks");
+  return (r / (256u / kRow)) & (kRow / 16u - 1u);
 }
 template <uint32_t kRow>
 __device__ __forceinline__ uint32_t mx_at(uint32_t r, uint32_t chunk) {
@@ -518,8 +520,8 @@ __device__ __forceinline__ uint32_t mx_turn_cols(uint32_t c) { return ((c & 3u) 
 // the 64 banks once.
 template <int kBits, uint32_t kRow>
 __device__ __forceinline__ uint32_t mx_turn_pairs(uint32_t r) {
-  static_assert(kRow == 128u || kRow == (kBits == 4 ? 64u : 256u), "tiles of 128 or 256 columns");
-  if (kBits == 8) return kRow == 128u ? (r >> 1 & 1u) << 2 : (r & 3u) << 2;
+  static_assert(kRow == 128u || (kRow == 64u && kBits == 4), "tiles of 128 or 256 columns, mx8 of 128");
+  if (kBits == 8) return (r >> 1 & 1u) << 2;
   return kRow == 128u ? (r >> 1 & 3u) << 1 : (r >> 2 & 1u) << 1;
 }
 
@@ -535,7 +537,7 @@ __device__ __forceinline__ v8bf mx_read_cols(const uint8_t* at0, const uint8_t* 
 }
 
 // The products on BF16 matrix instructions: tiles of kBM x kBN outputs, kWM x
-// kWN waves, 64 contraction values a step, a ring of kStages steps in LDS
+// kWN waves, kBC contraction values a step, a ring of kStages steps in LDS
 // filled by loads that need no registers, one barrier a step.  A wave keeps
 // its 32 x 32 sums in registers.
 //   matmul  M tokens, N weight rows, contraction k: both operands run along
@@ -556,8 +558,8 @@ __device__ __forceinline__ v8bf mx_read_cols(const uint8_t* at0, const uint8_t* 
 // their power leaves, then what a tile cannot hide (dx of 32,768 rows in one
 // group, n = k = 2,048: 258 us, 1.07 PFLOP/s; without its loads 25, conversions
 // 28, stores 20 us less).  Measured at n = 1,024, k = 2,048, 64 groups of 512
-// rows on average: dx 167 us, wgrad 220 us (268 MB of results, no tile shape
-// within 5 % of it faster); matmul of 4,001 x 2,048 x 2,048: 34 us.
+// rows on average: dx 161 us, wgrad 221 us (268 MB of results; 128 x 128, 128 x
+// 256 and 256 x 256 tiles within 5 %); matmul of 4,001 x 2,048 x 2,048: 35 us.
 template <int kOp, uint32_t kBM, uint32_t kBN, uint32_t kBC, uint32_t kWM, uint32_t kWN, uint32_t kStages, uint32_t kPerCu>
 __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_gemm(MxArgs p) {
   constexpr bool kRowsB = kOp == kMxMatmul || kOp == kMxMatmul8;  // B runs along the contraction
@@ -612,7 +614,7 @@ __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_
     c1 = mx_first(min(each, b - a - from));
   } else {
     MxTile t;
-    if (!mx_find_tile(p, kBM == 256u ? 8u : kBM == 128u ? 7u : kBM == 64u ? 6u : 5u, ntiles, t)) return;
+    if (!mx_find_tile(p, kBM == 128u ? 7u : kBM == 64u ? 6u : 5u, ntiles, t)) return;
     g = t.g;
     m0 = t.row0;
     m1 = t.row1;
@@ -937,7 +939,9 @@ __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_
 // by 1/7 of a BF16 rounding at the most; where the caller asks for FP32 it
 // would show, and k_mx_gemm computes that.  128 contraction values (four
 // blocks) a step, the ring and the tile as in k_mx_gemm; the padded pitch
-// leaves no partial step.
+// leaves no partial step.  8,192 rows in 64 groups, n = 1,024, k = 2,048: 35
+// us, to FP32 by k_mx_gemm 51; 32,768 rows: 87 us, 1.57 PFLOP/s, bound by what
+// its loads keep in flight, 43 KB a CU.
 template <uint32_t kBM, uint32_t kBN, uint32_t kWM, uint32_t kWN, uint32_t kStages, uint32_t kPerCu>
 __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_gemm8(MxArgs p) {
   constexpr uint32_t kW = kWM * kWN;
@@ -955,7 +959,7 @@ __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_
   const uint32_t wave = uint32_t(__builtin_amdgcn_readfirstlane(int(tid >> 6)));
   if (blockIdx.x == 0u) mx_report(p);
   MxTile t;
-  if (!mx_find_tile(p, kBM == 256u ? 8u : kBM == 128u ? 7u : kBM == 64u ? 6u : 5u, (p.n + kBN - 1u) / kBN, t)) return;
+  if (!mx_find_tile(p, kBM == 128u ? 7u : kBM == 64u ? 6u : 5u, (p.n + kBN - 1u) / kBN, t)) return;
   const uint32_t m0 = t.row0, m1 = t.row1, n0 = t.col * kBN;
   const uint32_t lds0 = mx_lds(lds);
 
@@ -1320,7 +1324,7 @@ ciera_status mx_encode_impl(const void* d_x, uint64_t rows, uint64_t cols, uint6
   const uint64_t at = mx_scales_at(rows, cols, kBits);
   const uint64_t units = rows * (mx_pitch(cols) / 8u);
   const uint64_t grid = cdiv(units, kMxThreads * kMxUnits);
-  if (grid > 0x7FFFFFFFu) return CIERA_ERR_ARG;
+  if (grid * kMxThreads > kMxMostThreads) return CIERA_ERR_ARG;
   uint8_t* q = static_cast<uint8_t*>(d_q);
   (void)hipGetLastError();
   launch(k_mx_encode<kBits>, dim3(uint32_t(grid)), dim3(kMxThreads), stream, static_cast<const uint16_t*>(d_x), rows,
@@ -1335,7 +1339,7 @@ ciera_status mx_decode_impl(const void* d_q, uint64_t q_bytes, uint64_t rows, ui
   if (st == CIERA_OK) st = mx_encoded(d_q, q_bytes, rows, cols, kBits, CIERA_ERR_FORMAT);
   if (st != CIERA_OK || !rows || !cols) return st;
   const uint64_t grid = cdiv(rows * cdiv(cols, 8u), kMxThreads * kMxUnits);
-  if (grid > 0x7FFFFFFFu) return CIERA_ERR_ARG;
+  if (grid * kMxThreads > kMxMostThreads) return CIERA_ERR_ARG;
   const uint8_t* q = static_cast<const uint8_t*>(d_q);
   (void)hipGetLastError();
   launch(k_mx_decode<kBits>, dim3(uint32_t(grid)), dim3(kMxThreads), stream, q, q + mx_scales_at(rows, cols, kBits),
@@ -1414,14 +1418,14 @@ ciera_status mx_gemm_as(const MxArgs& p, hipStream_t stream) {
   constexpr bool kRowsB = kOp == kMxMatmul || kOp == kMxMatmul8;
   const uint64_t mtiles = kOp == kMxWgrad ? cdiv(p.n, kBM) * p.groups * p.parts : mx_token_tiles(p, kBM);
   const uint64_t grid = mtiles * cdiv(kRowsB ? p.n : p.k, kBN);
-  if (grid > 0x7FFFFFFFu) return CIERA_ERR_ARG;
+  if (grid * (kWM * kWN * 64u) > kMxMostThreads) return CIERA_ERR_ARG;
   launch(k_mx_gemm<kOp, kBM, kBN, kBC, kWM, kWN, kStages, kPerCu>, dim3(uint32_t(grid), kOp == kMxDx ? p.parts : 1u), dim3(kWM * kWN * 64u), stream, p);
   return launch_status();
 }
 template <uint32_t kBM, uint32_t kBN, uint32_t kWM, uint32_t kWN, uint32_t kStages, uint32_t kPerCu>
 ciera_status mx_gemm8_as(const MxArgs& p, hipStream_t stream) {
   const uint64_t grid = mx_token_tiles(p, kBM) * cdiv(p.n, kBN);
-  if (grid > 0x7FFFFFFFu) return CIERA_ERR_ARG;
+  if (grid * (kWM * kWN * 64u) > kMxMostThreads) return CIERA_ERR_ARG;
   launch(k_mx_gemm8<kBM, kBN, kWM, kWN, kStages, kPerCu>, dim3(uint32_t(grid)), dim3(kWM * kWN * 64u), stream, p);
   return launch_status();
 }
