@@ -1107,14 +1107,14 @@ __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_
 //             fill the chip otherwise.
 // 64 rows on 42 of 64 groups of 1,024 x 2,048: 13.3 us for 47 MB, 3.5 TB/s;
 // one row, n = k = 2,048: 6.9 us, a launch.  Its time grows with the outputs,
-// the tiles' does not until they fill the chip: taken up to kMxFewOutputs (16
-// rows, n = 2,048: 7.9 against 12.5 us; 32 rows: 9.6 against 12.5; 8 rows, n =
-// 16,384: 12.7 against 12.9; 16 rows: 15.7 against 13.0; 64 groups, n = 1,024,
-// 128 rows: 16.5 against 17.6, 512 rows: 25 against 18).  x in mx8 with a BF16
+// the tiles' does not until they fill the chip: taken below kMxFewOutputs (16
+// rows, n = 2,048: 7.9 against 12.5 us; 32 rows: 9.6 against 12.5; 64 rows: 16.5
+// against 12.6; 8 rows, n = 16,384: 12.7 against 12.9; 64 groups, n = 1,024, 64
+// rows: 15.2 against 17.7, 512 rows: 25 against 18).  x in mx8 with a BF16
 // result goes to the scaled instructions at any size (n = 2,048, one row: 8.8
 // against 8.3 us; 64 rows in 64 groups: 13.4 against 16.3).
 constexpr uint32_t kMxFewThreads = 512u;
-constexpr uint64_t kMxFewOutputs = 1u << 17;  // the most outputs (all tokens' n) for which it is taken
+constexpr uint64_t kMxFewOutputs = 1u << 17;  // outputs (all tokens' n) below which it is taken
 
 // Eight values of x, c a multiple of 8: as loaded (mx8: the values, then the
 // scale byte), and as BF16.  Behind the contraction's end: zeros.
@@ -1438,9 +1438,10 @@ ciera_status mx_gemm8_as(const MxArgs& p, hipStream_t stream) {
 //   matmul  32 or 64 rows: 1,024: 18.0, 18.7; 2,048: 34, 25; 2,000 in 64 g: 25, 27.5; 5,000 in 64 g: 47, 40.
 //           64 or 128 rows: 3,000: 32, 34; 4,096: 46, 37; 6,000 in 64 g: 43, 46; 8,192 in 64 g: 55, 48.
 //           128 rows, 128 or 256 columns: 4,001: 37, 41; 8,192: 72, 69; 32,768: 265, 252.
-//           x in mx8, BF16 result (the scaled instructions), 32 or 64 rows: 2,048: 21, 16; 2,000 in 64 g: 17.5, 23;
-//           6,000 in 64 g: 32, 29; 64 or 128 rows: 3,000: 24, 24; 8,192: 56, 44; 6,000 in 64 g: 29, 34.
+//           x in mx8, BF16 result (the scaled instructions), 32 or 64 rows: 2,048: 21, 16; 2,000 in 64 g: 17, 23;
+//           6,000 in 64 g: 32, 30; 64 or 128 rows: 3,000: 24, 24; 8,192: 56, 44; 6,000 in 64 g: 30, 34.
 //   dx      64 x 128 or 64 x 256: 512: 23, 29; 2,048: 34, 33; 64 in 64 g: 27, 22; 4,000 in 64 g: 40, 32.
+//           32 or 64 rows of 256: 999 in 66 g with n = 1,408: 27, 31; 500 in 64 g: 18, 22; 3,000: 30, 31; 4,000: 36, 33.
 //           64 or 128 rows: 4,096: 49, 47; 8,192: 79, 73; 32,768: 277, 258; 8,192 in 8 g: 50, 52; 32,768 in 64 g: 167, 170.
 template <int kOp>
 ciera_status mx_gemm(const MxArgs& p, hipStream_t stream) {
@@ -1448,6 +1449,7 @@ ciera_status mx_gemm(const MxArgs& p, hipStream_t stream) {
     if (mx_rows_each(p) >= 1024u && mx_tiles(p, p.k) >= 2u * kMxCus)
       return mx_gemm_as<kOp, 128u, 256u, 64u, 1u, 4u, 3u, 2u>(p, stream);
     if (mx_token_tiles(p, 64u) * cdiv(p.k, 128u) <= 2u * kMxCus) return mx_gemm_as<kOp, 64u, 128u, 64u, 2u, 2u, 3u, 2u>(p, stream);
+    if (mx_rows_each(p) <= 48u) return mx_gemm_as<kOp, 32u, 256u, 64u, 1u, 4u, 2u, 4u>(p, stream);
     return mx_gemm_as<kOp, 64u, 256u, 64u, 1u, 4u, 2u, 3u>(p, stream);
   } else {
     const uint64_t tiles = mx_tiles(p, p.n);
@@ -1461,7 +1463,7 @@ ciera_status mx_gemm(const MxArgs& p, hipStream_t stream) {
 ciera_status mx_gemm8(const MxArgs& p, hipStream_t stream) {
   const uint64_t tiles = mx_tiles(p, p.n);
   if (mx_rows_each(p) > 64u && tiles > 3u * kMxCus / 4u) return mx_gemm8_as<128u, 256u, 2u, 2u, 2u, 2u>(p, stream);
-  if (mx_rows_each(p) > 48u && tiles > kMxCus / 4u) return mx_gemm8_as<64u, 128u, 1u, 4u, 3u, 2u>(p, stream);
+  if (mx_rows_each(p) > 48u && tiles > kMxCus / 4u) return mx_gemm8_as<64u, 128u, 1u, 4u, 2u, 4u>(p, stream);
   return mx_gemm8_as<32u, 128u, 1u, 4u, 3u, 2u>(p, stream);
 }
 
@@ -1473,7 +1475,7 @@ ciera_status mx_matmul_impl(MxArgs& p, hipStream_t stream) {
     return launch_status();
   }
   if (kMx8 && !p.out_f32) return mx_gemm8(p, stream);
-  if (uint64_t(p.tokens) * p.n <= kMxFewOutputs) {
+  if (uint64_t(p.tokens) * p.n < kMxFewOutputs) {
     // 128 rows a workgroup once that gives every other CU one (one token,
     // k = 2,048: n = 8,192: 9.0 against 8.2 us, 16,384: 8.8 against 11.0)
     const uint64_t live = p.groups < p.tokens ? p.groups : p.tokens;
