@@ -558,7 +558,7 @@ __device__ __forceinline__ v8bf mx_read_cols(const uint8_t* at0, const uint8_t* 
 // their power leaves, then what a tile cannot hide (dx of 32,768 rows in one
 // group, n = k = 2,048: 258 us, 1.07 PFLOP/s; without its loads 25, conversions
 // 28, stores 20 us less).  Measured at n = 1,024, k = 2,048, 64 groups of 512
-// rows on average: dx 161 us, wgrad 221 us (268 MB of results; 128 x 128, 128 x
+// rows on average: dx 161 us, wgrad 202 us (268 MB of results; 128 x 128, 128 x
 // 256 and 256 x 256 tiles within 5 %); matmul of 4,001 x 2,048 x 2,048: 35 us.
 template <int kOp, uint32_t kBM, uint32_t kBN, uint32_t kBC, uint32_t kWM, uint32_t kWN, uint32_t kStages, uint32_t kPerCu>
 __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_gemm(MxArgs p) {
@@ -598,13 +598,25 @@ __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_
   uint32_t r0 = 0u, part = 0u;  // first contraction row, and which part of them (wgrad; dx: of n)
   if constexpr (kOp == kMxWgrad) {
     const uint32_t mtiles = (p.n + kBM - 1u) / kBM;
-    const uint32_t at = mx_xcd_run(blockIdx.x, gridDim.x);
-    const uint32_t gp = at / (mtiles * ntiles);
-    const uint32_t t = at - gp * (mtiles * ntiles);
+    const uint32_t all = mtiles * ntiles;  // of a group's part
+    uint32_t gp, t;
+    if (p.groups > 1u) {
+      // a tile takes as long as its group has rows, so each XCD takes an
+      // eighth of every group's tiles, the odd ones in turn (64 groups of 512
+      // rows on average: 204 us, whole groups an XCD 219)
+      const uint32_t per = (all + 7u) / 8u, at = blockIdx.x >> 3;
+      gp = at / per;
+      t = ((blockIdx.x + gp) & 7u) * per + at % per;
+      if (t >= all) return;
+    } else {
+      const uint32_t at = mx_xcd_run(blockIdx.x, gridDim.x);
+      gp = at / all;
+      t = at - gp * all;
+    }
     part = gp / p.groups;
     g = gp - part * p.groups;
-    m0 = (t % mtiles) * kBM;
-    n0 = (t / mtiles) * kBN;
+    m0 = t / ntiles * kBM;
+    n0 = (t % ntiles) * kBN;
     m1 = p.n;
     uint32_t a, b;
     mx_rows(p, g, a, b);
@@ -1416,8 +1428,13 @@ uint32_t mx_rows_each(const MxArgs& p) { return p.tokens / p.groups; }
 template <int kOp, uint32_t kBM, uint32_t kBN, uint32_t kBC, uint32_t kWM, uint32_t kWN, uint32_t kStages, uint32_t kPerCu>
 ciera_status mx_gemm_as(const MxArgs& p, hipStream_t stream) {
   constexpr bool kRowsB = kOp == kMxMatmul || kOp == kMxMatmul8;
-  const uint64_t mtiles = kOp == kMxWgrad ? cdiv(p.n, kBM) * p.groups * p.parts : mx_token_tiles(p, kBM);
-  const uint64_t grid = mtiles * cdiv(kRowsB ? p.n : p.k, kBN);
+  const uint64_t ntiles = cdiv(kRowsB ? p.n : p.k, kBN);
+  uint64_t grid = mx_token_tiles(p, kBM) * ntiles;
+  if (kOp == kMxWgrad) {
+    grid = cdiv(p.n, kBM) * ntiles;
+    if (p.groups > 1u) grid = cdiv(grid, 8u) * 8u;
+    grid *= p.groups * p.parts;
+  }
   if (grid * (kWM * kWN * 64u) > kMxMostThreads) return CIERA_ERR_ARG;
   launch(k_mx_gemm<kOp, kBM, kBN, kBC, kWM, kWN, kStages, kPerCu>, dim3(uint32_t(grid), kOp == kMxDx ? p.parts : 1u), dim3(kWM * kWN * 64u), stream, p);
   return launch_status();
