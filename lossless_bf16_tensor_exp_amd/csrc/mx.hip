@@ -558,7 +558,7 @@ __device__ __forceinline__ v8bf mx_read_cols(const uint8_t* at0, const uint8_t* 
 // their power leaves, then what a tile cannot hide (dx of 32,768 rows in one
 // group, n = k = 2,048: 258 us, 1.07 PFLOP/s; without its loads 25, conversions
 // 28, stores 20 us less).  Measured at n = 1,024, k = 2,048, 64 groups of 512
-// rows on average: dx 161 us, wgrad 202 us (268 MB of results; 128 x 128, 128 x
+// rows on average: dx 156 us, wgrad 205 us (268 MB of results; 128 x 128, 128 x
 // 256 and 256 x 256 tiles within 5 %); matmul of 4,001 x 2,048 x 2,048: 35 us.
 template <int kOp, uint32_t kBM, uint32_t kBN, uint32_t kBC, uint32_t kWM, uint32_t kWN, uint32_t kStages, uint32_t kPerCu>
 __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_gemm(MxArgs p) {
@@ -952,8 +952,9 @@ __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_
 // would show, and k_mx_gemm computes that.  128 contraction values (four
 // blocks) a step, the ring and the tile as in k_mx_gemm; the padded pitch
 // leaves no partial step.  8,192 rows in 64 groups, n = 1,024, k = 2,048: 35
-// us, to FP32 by k_mx_gemm 51; 32,768 rows: 87 us, 1.57 PFLOP/s, bound by what
-// its loads keep in flight, 43 KB a CU.
+// us, to FP32 by k_mx_gemm 51; 32,768 rows: 84 us, 1.64 PFLOP/s, bound by what
+// its loads keep in flight, 43 KB a CU.  A row's four scale bytes of a step are
+// read as one word (byte by byte: 87 us).
 template <uint32_t kBM, uint32_t kBN, uint32_t kWM, uint32_t kWN, uint32_t kStages, uint32_t kPerCu>
 __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_gemm8(MxArgs p) {
   constexpr uint32_t kW = kWM * kWN;
@@ -1054,21 +1055,21 @@ __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_
     const uint8_t* s_a = lds + slot * kStage;
     const uint8_t* s_b = s_a + kABytes;
     const uint32_t chunk = step / 4u;
-    const uint8_t* s_s = lds + scales_at(chunk) + (step % 4u) * 4u + half;
+    const uint8_t* s_s = lds + scales_at(chunk) + (step % 4u) * 4u;
     // Lane half h holds block 2 s + h of B's row, and of A's row the 16
     // values at 16 h and at 32 + 16 h of the 64; its scale byte is block
-    // 2 s + h's.  Both bytes of a step sit in one word, the instruction picks
-    // byte 0 or 2 of it.
+    // 2 s + h's.  A step's four bytes of a row are one word; turned by the
+    // half, the instruction picks byte 0 or 2 of it.
     uint32_t sa[kFM], sb[kFN];
 #pragma unroll
     for (uint32_t i = 0; i < kFM; i++) {
       const uint8_t* at = s_s + (kBN + wm + i * kMStep + (lane & 31u)) * 16u + late(left_a[i], chunk);
-      sa[i] = at[0] | uint32_t(at[2]) << 16;
+      sa[i] = *reinterpret_cast<const uint32_t*>(at) >> (8u * half);
     }
 #pragma unroll
     for (uint32_t j = 0; j < kFN; j++) {
       const uint8_t* at = s_s + (wn + j * 32u + (lane & 31u)) * 16u + late(left_b[j], chunk);
-      sb[j] = at[0] | uint32_t(at[2]) << 16;
+      sb[j] = *reinterpret_cast<const uint32_t*>(at) >> (8u * half);
     }
 #pragma unroll
     for (uint32_t s = 0; s < 2u; s++) {
