@@ -103,13 +103,15 @@ class MxLinear:
     checkpoint of x: one linear layer, or with ``offsets`` (groups + 1 row
     numbers) the experts of a mixture-of-experts layer, whose groups (n, k)
     matrices lie one behind the other.  Takes up to ``tokens`` rows a call.
+    With ``scaled``, ``keep`` takes a BF16 y from the scaled matrix
+    instructions (``mx4_matmul_mx8``: faster, less exact than an FP32 sum).
 
     ``keep`` and the calls that read the checkpoint share one buffer, so one
     layer's forward and backward belong to one stream, or are ordered by the
     caller.  ``backward`` takes the offsets its ``keep`` had."""
 
-    def __init__(self, tokens: int, n: int, k: int, groups: int = 1, device="cuda"):
-        self.tokens, self.n, self.k, self.groups = tokens, n, k, groups
+    def __init__(self, tokens: int, n: int, k: int, groups: int = 1, device="cuda", scaled: bool = False):
+        self.tokens, self.n, self.k, self.groups, self.scaled = tokens, n, k, groups, scaled
         size = mx_workspace_size(tokens, n, k, groups)
         if size == 0:
             raise ValueError(f"no workspace for {tokens} x {n} x {k} in {groups} groups")
@@ -147,7 +149,8 @@ class MxLinear:
         if tuple(x.shape) != (y.shape[0], self.k):
             raise ValueError(f"x is {tuple(x.shape)}, the product's ({y.shape[0]}, {self.k})")
         mx8_encode(x, self.xq, stream)
-        mx4_matmul_mx8(self.xq, self.k, self.w, y, self.ws, offsets, stream)
+        mx4_matmul_mx8(self.xq, self.k, self.w, y, self.ws, offsets, stream,
+                       self.scaled and y.dtype is not torch.float32)
         self.kept = x.shape[0]
 
     def backward(self, dy, dx, dw, offsets=None, accumulate: bool = False, stream=None):

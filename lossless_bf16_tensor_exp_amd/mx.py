@@ -8,7 +8,7 @@ on them.
     mx8_decode(inp, y, stream=None)       mx4_decode(inp, y, stream=None)
     mx_workspace_size(tokens, n, k, groups=1)
     mx4_matmul(x, w, y, ws, offsets=None, stream=None)                 y = x W^T
-    mx4_matmul_mx8(xq, k, w, y, ws, offsets=None, stream=None)         y = x W^T, x in mx8
+    mx4_matmul_mx8(xq, k, w, y, ws, offsets=None, stream=None, scaled=False)   y = x W^T, x in mx8
     mx4_matmul_dx(dy, w, dx, ws, offsets=None, stream=None)            dx = dy W
     mx8_wgrad(dy, xq, dw, ws, offsets=None, accumulate=False, stream=None)   dW = dy^T x
 
@@ -32,6 +32,7 @@ from . import _raise, load_library
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
 _f32, _i64, _u8 = torch.float32, torch.int64, torch.uint8
 _vp, _u64, _u32, _i32 = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint32, ctypes.c_int
+_SCALED = 4  # CIERA_MX_SCALED
 _bound = None
 _current_device = torch.cuda.current_device
 # the current stream's handle without the Stream object around it (1 us a call)
@@ -160,9 +161,10 @@ def _groups(offsets):
     return offsets.numel() - 1, offsets.data_ptr(), (offsets,)
 
 
-def _product(name, a, lead, width, w, out, ws, offsets, tokens, n, k, stream):
+def _product(name, a, lead, width, w, out, ws, offsets, tokens, n, k, stream, bf16=0):
     """One call of a matmul-shaped entry point; ``lead`` is its left operand's
-    pointer and stride or size, ``width`` the output's columns."""
+    pointer and stride or size, ``width`` the output's columns, ``bf16`` what a
+    BF16 output is asked for with."""
     rows, cols, ldo = _rows(out, "the output", f32=True)
     if rows != tokens or cols != width:
         raise ValueError(f"the output is {rows} x {cols}, the product {tokens} x {width}")
@@ -170,7 +172,7 @@ def _product(name, a, lead, width, w, out, ws, offsets, tokens, n, k, stream):
     sp, sn = _bytes(ws, "ws")
     groups, offs, table = _groups(offsets)
     _call(name, out.get_device(), (a, w, ws, *table), stream, *lead, wp, wn, out.data_ptr(), ldo,
-          1 if out.dtype is _f32 else 0, tokens, n, k, groups, offs, sp, sn)
+          1 if out.dtype is _f32 else bf16, tokens, n, k, groups, offs, sp, sn)
 
 
 def mx4_matmul(x, w, y, ws, offsets=None, stream=None) -> None:
@@ -181,12 +183,17 @@ def mx4_matmul(x, w, y, ws, offsets=None, stream=None) -> None:
     _product("mx4_matmul", x, (x.data_ptr(), ldx), n, w, y, ws, offsets, tokens, n, k, stream)
 
 
-def mx4_matmul_mx8(xq, k: int, w, y, ws, offsets=None, stream=None) -> None:
-    """y = x W^T with x (y's rows, k) in mx8."""
+def mx4_matmul_mx8(xq, k: int, w, y, ws, offsets=None, stream=None, scaled: bool = False) -> None:
+    """y = x W^T with x (y's rows, k) in mx8.  ``scaled`` (y in BF16) takes the
+    scaled matrix instructions: faster on many rows, and within each block of
+    32 they cut what lies below 2^-13 of the largest product."""
     if y.dim() != 2:
         raise ValueError("the output must be a two-dimensional device tensor")
+    if scaled and y.dtype is _f32:
+        raise ValueError("the scaled matrix instructions are for a BF16 output")
     tokens, n = y.shape
-    _product("mx4_matmul_mx8", xq, _bytes(xq, "xq"), n, w, y, ws, offsets, tokens, n, k, stream)
+    _product("mx4_matmul_mx8", xq, _bytes(xq, "xq"), n, w, y, ws, offsets, tokens, n, k, stream,
+             _SCALED if scaled else 0)
 
 
 def mx4_matmul_dx(dy, w, dx, ws, offsets=None, stream=None) -> None:
