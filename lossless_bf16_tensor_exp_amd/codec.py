@@ -127,9 +127,18 @@ class MxLinear:
             raise ValueError(f"weights are {tuple(weights.shape)}, the layer's ({self.groups}, {self.n}, {self.k})")
         mx4_encode(rows, self.w, stream)
 
-    def _rows(self, rows: int):
+    def _shape(self, name: str, t, *wanted):
+        """The calls take n and k from their tensors, and would read the layer's buffers as those of a smaller matrix."""
+        if tuple(t.shape) not in wanted:
+            raise ValueError(f"{name} is {tuple(t.shape)}, the layer's {' or '.join(map(str, wanted))}")
+
+    def _product(self, x, y, offsets):
+        rows = x.shape[0]
         if rows > self.tokens:
             raise ValueError(f"{rows} rows in a layer made for {self.tokens}")
+        self._shape("x", x, (rows, self.k))
+        self._shape("y", y, (rows, self.n))
+        self._table(offsets)
 
     def _table(self, offsets):
         if (1 if offsets is None else offsets.numel() - 1) != self.groups:
@@ -137,17 +146,13 @@ class MxLinear:
 
     def forward(self, x, y, offsets=None, stream=None):
         """y = x W^T; nothing is kept."""
-        self._rows(x.shape[0])
-        self._table(offsets)
+        self._product(x, y, offsets)
         mx4_matmul(x, self.w, y, self.ws, offsets, stream)
 
     def keep(self, x, y, offsets=None, stream=None):
         """The checkpoint of x into ``xq``, and y from it: what ``backward``
         sees is what the product took."""
-        self._rows(x.shape[0])
-        self._table(offsets)
-        if tuple(x.shape) != (y.shape[0], self.k):
-            raise ValueError(f"x is {tuple(x.shape)}, the product's ({y.shape[0]}, {self.k})")
+        self._product(x, y, offsets)
         mx8_encode(x, self.xq, stream)
         mx4_matmul_mx8(self.xq, self.k, self.w, y, self.ws, offsets, stream,
                        self.scaled and y.dtype is not torch.float32)
@@ -159,6 +164,12 @@ class MxLinear:
         self._table(offsets)
         if dy.shape[0] != self.kept:
             raise ValueError(f"{dy.shape[0]} rows of dy for a checkpoint of {self.kept}")
+        self._shape("dy", dy, (self.kept, self.n))
+        if dx is not None:
+            self._shape("dx", dx, (self.kept, self.k))
+        if dw is not None:
+            stack = (self.groups, self.n, self.k)
+            self._shape("dw", dw, stack, *([stack[1:]] if self.groups == 1 else []))
         if dx is not None:
             mx4_matmul_dx(dy, self.w, dx, self.ws, offsets, stream)
         if dw is not None:

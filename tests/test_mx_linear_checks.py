@@ -1,0 +1,73 @@
+"""What MxLinear refuses, without a GPU: the library's calls are replaced by
+ones that record that they were reached."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+CALLS = ("mx4_encode", "mx4_matmul", "mx8_encode", "mx4_matmul_mx8", "mx4_matmul_dx", "mx8_wgrad")
+
+
+@pytest.fixture
+def made(monkeypatch):
+    """make(...) a layer on the CPU; made.reached lists the calls it made."""
+    from lossless_bf16_tensor_exp_amd import codec
+
+    class Made:
+        reached, fails = [], set()
+
+        def __call__(self, *args, **kw):
+            return codec.MxLinear(*args, device="cpu", **kw)
+
+    made = Made()
+    made.reached, made.fails = [], set()
+    for name in CALLS:
+        def call(*args, name=name, **kw):
+            made.reached.append(name)
+            if name in made.fails:
+                raise TypeError(name)
+        monkeypatch.setattr(codec, name, call)
+    return made
+
+
+def bf(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("x,y", [((8, 128), (8, 64)), ((8, 256), (8, 32)), ((8, 256), (8, 65)), ((8, 257), (8, 64)),
+                                 ((8, 256), (7, 64)), ((64, 256), (64, 64)), ((8,), (8, 64)), ((8, 256), (8,)),
+                                 ((1, 8, 256), (8, 64))])
+def test_forward_and_keep_take_the_layers_shapes_only(made, x, y):
+    layer = made(16, 64, 256)
+    for call in (layer.forward, layer.keep):
+        with pytest.raises(ValueError):
+            call(bf(*x), bf(*y))
+    assert made.reached == []
+    layer.forward(bf(8, 256), bf(8, 64))
+    layer.keep(bf(8, 256), bf(8, 64))
+    assert made.reached == ["mx4_matmul", "mx8_encode", "mx4_matmul_mx8"]
+
+
+@pytest.mark.parametrize("groups,dy,dx,dw", [(1, (8, 32), None, (64, 256)), (1, (8, 64), (8, 128), None),
+                                             (1, (8, 64), (7, 256), None), (1, (8, 64), None, (64, 128)),
+                                             (1, (8, 64), None, (32, 256)), (1, (8, 64), None, (2, 64, 256)),
+                                             (2, (8, 64), None, (64, 256)), (2, (8, 64), None, (2, 64, 128)),
+                                             (2, (8, 32), (8, 256), (2, 32, 256)), (1, (7, 64), (7, 256), None),
+                                             (1, (8,), (8, 256), None), (1, (8, 64), (8, 256), (64, 255))])
+def test_backward_takes_the_layers_shapes_only(made, groups, dy, dx, dw):
+    layer = made(16, 64, 256, groups)
+    offsets = None if groups == 1 else torch.tensor([0, 3, 8])
+    layer.keep(bf(8, 256), bf(8, 64), offsets)
+    del made.reached[:]
+    with pytest.raises(ValueError):
+        layer.backward(bf(*dy), None if dx is None else bf(*dx), None if dw is None else bf(*dw), offsets)
+    assert made.reached == [], "a refused call computes neither gradient"
+    layer.backward(bf(8, 64), bf(8, 256), bf(groups, 64, 256), offsets)
+    assert made.reached == ["mx4_matmul_dx", "mx8_wgrad"]
+
+
+def test_one_groups_gradient_has_two_or_three_dimensions(made):
+    layer = made(16, 64, 256)
+    layer.keep(bf(8, 256), bf(8, 64))
+    layer.backward(bf(8, 64), None, bf(64, 256))
+    layer.backward(bf(8, 64), None, bf(1, 64, 256))
+    assert made.reached[-2:] == ["mx8_wgrad"] * 2
