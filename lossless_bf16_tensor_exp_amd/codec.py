@@ -118,7 +118,7 @@ class MxLinear:
         self.w = torch.empty(mx4_encoded_size(groups * n, k), dtype=torch.uint8, device=device)
         self.xq = torch.empty(mx8_encoded_size(tokens, k), dtype=torch.uint8, device=device)
         self.ws = torch.empty(size, dtype=torch.uint8, device=device)
-        self.kept = 0
+        self.kept = None  # rows of the checkpoint in xq, None while there is none
 
     def load(self, weights, stream=None):
         """The BF16 weights, (n, k) or (groups, n, k), into ``w``."""
@@ -153,6 +153,7 @@ class MxLinear:
         """The checkpoint of x into ``xq``, and y from it: what ``backward``
         sees is what the product took."""
         self._product(x, y, offsets)
+        self.kept = None  # until both calls are made: the first one overwrites xq
         mx8_encode(x, self.xq, stream)
         mx4_matmul_mx8(self.xq, self.k, self.w, y, self.ws, offsets, stream,
                        self.scaled and y.dtype is not torch.float32)
@@ -163,7 +164,8 @@ class MxLinear:
         either output may be None."""
         self._table(offsets)
         if dy.shape[0] != self.kept:
-            raise ValueError(f"{dy.shape[0]} rows of dy for a checkpoint of {self.kept}")
+            raise ValueError(f"{dy.shape[0]} rows of dy for " +
+                             ("no checkpoint" if self.kept is None else f"a checkpoint of {self.kept}"))
         self._shape("dy", dy, (self.kept, self.n))
         if dx is not None:
             self._shape("dx", dx, (self.kept, self.k))

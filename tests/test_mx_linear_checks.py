@@ -71,3 +71,29 @@ def test_one_groups_gradient_has_two_or_three_dimensions(made):
     layer.backward(bf(8, 64), None, bf(64, 256))
     layer.backward(bf(8, 64), None, bf(1, 64, 256))
     assert made.reached[-2:] == ["mx8_wgrad"] * 2
+
+
+def test_a_keep_that_fails_leaves_no_checkpoint(made):
+    """The new x overwrites the buffer before the product can refuse: what an earlier call kept is gone then."""
+    layer = made(16, 64, 256)
+    for call in ("mx4_matmul_mx8", "mx8_encode"):
+        layer.keep(bf(8, 256), bf(8, 64))
+        layer.backward(bf(8, 64), None, bf(64, 256))
+        made.fails = {call}
+        with pytest.raises(TypeError):
+            layer.keep(bf(12, 256), bf(12, 64))
+        del made.reached[:]
+        for rows in (8, 12, 0):
+            with pytest.raises(ValueError):
+                layer.backward(bf(rows, 64), bf(rows, 256), bf(64, 256))
+        assert made.reached == []
+        made.fails = set()
+
+
+def test_backward_needs_a_checkpoint(made):
+    layer = made(16, 64, 256)
+    with pytest.raises(ValueError):
+        layer.backward(bf(0, 64), None, bf(64, 256))
+    layer.keep(bf(0, 256), bf(0, 64))
+    layer.backward(bf(0, 64), None, bf(64, 256))
+    assert made.reached[-1] == "mx8_wgrad"
