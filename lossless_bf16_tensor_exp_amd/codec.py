@@ -121,10 +121,15 @@ class MxLinear:
         self.kept = None  # rows of the checkpoint in xq, None while there is none
 
     def load(self, weights, stream=None):
-        """The BF16 weights, (n, k) or (groups, n, k), into ``w``."""
-        rows = weights.reshape(-1, weights.shape[-1]) if weights.is_contiguous() else weights
-        if tuple(rows.shape) != (self.groups * self.n, self.k):
-            raise ValueError(f"weights are {tuple(weights.shape)}, the layer's ({self.groups}, {self.n}, {self.k})")
+        """The BF16 weights, (groups, n, k) or their rows one behind the other,
+        (groups * n, k), into ``w``.  Rows may lie further apart than k, the
+        same everywhere."""
+        flat = (self.groups * self.n, self.k)
+        self._shape("the weights", weights, (self.groups, self.n, self.k), flat)
+        try:
+            rows = weights.view(flat)
+        except RuntimeError:
+            raise ValueError(f"the weights' rows do not lie equally far apart: strides {weights.stride()}") from None
         mx4_encode(rows, self.w, stream)
 
     def _shape(self, name: str, t, *wanted):

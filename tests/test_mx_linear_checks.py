@@ -97,3 +97,26 @@ def test_backward_needs_a_checkpoint(made):
     layer.keep(bf(0, 256), bf(0, 64))
     layer.backward(bf(0, 64), None, bf(64, 256))
     assert made.reached[-1] == "mx8_wgrad"
+
+
+def test_load_takes_weights_that_lie_apart(made, monkeypatch):
+    """Rows of a wider buffer, in two dimensions or three; a copy is never made in silence."""
+    from lossless_bf16_tensor_exp_amd import codec
+    seen = []
+    monkeypatch.setattr(codec, "mx4_encode", lambda rows, out, stream=None: seen.append((rows.shape, rows.stride(), rows.data_ptr())))
+    layer = made(16, 64, 256, 3)
+    wide = torch.zeros(3, 64, 300, dtype=torch.bfloat16)
+    for w, stride in ((wide[:, :, :256], 300), (wide[:, :, 8:264], 300), (wide.view(192, 300)[:, :256], 300),
+                      (torch.zeros(3, 64, 256, dtype=torch.bfloat16), 256)):
+        layer.load(w)
+        assert seen[-1] == ((192, 256), (stride, 1), w.data_ptr())
+    for w in (torch.zeros(3, 70, 256, dtype=torch.bfloat16)[:, :64], torch.zeros(64, 3, 256, dtype=torch.bfloat16).transpose(0, 1)):
+        with pytest.raises(ValueError, match="apart"):
+            layer.load(w)
+    for shape in ((2, 64, 256), (64, 256), (3, 64, 255), (3, 1, 64, 256), (192 * 256,)):
+        with pytest.raises(ValueError):
+            layer.load(bf(*shape))
+    assert len(seen) == 4
+    one = made(16, 1, 256, 3)  # a row a group, each from a matrix of its own
+    one.load(torch.zeros(3, 5, 256, dtype=torch.bfloat16)[:, 2:3])
+    assert seen[-1][:2] == ((3, 256), (1280, 1))
