@@ -478,15 +478,20 @@ enum MxOp { kMxMatmul = 0, kMxDx = 1, kMxWgrad = 2, kMxMatmul8 = 3 };
 
 // Loads from global memory straight into LDS: lane i's 16 (or 4) bytes at
 // base + off land at lds + 16 i (4 i).  No register holds them, so they stay
-// in flight over whole steps; mx_fence counts them.
+// in flight over whole steps; mx_fence counts them.  m0 is named as written, so
+// that no use of it by the compiler is torn apart; the warning that it is a
+// reserved register says that it may not be kept, which is meant.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void mx_dma16(uint32_t off, const void* base, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
-               :: "v"(off), "s"(base), "s"(lds) : "memory");
+               :: "v"(off), "s"(base), "s"(lds) : "memory", "m0");
 }
 __device__ __forceinline__ void mx_dma4(uint32_t off, const void* base, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
-               :: "v"(off), "s"(base), "s"(lds) : "memory");
+               :: "v"(off), "s"(base), "s"(lds) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 // All but this wave's last kLeft loads have landed, its LDS reads and writes
 // are done, and so are every other wave's.
 template <int kLeft>
