@@ -15,6 +15,7 @@
 // (g+1) n - 1 of W.  A pair that decreases or leaves 0 .. tokens holds no
 // rows; workgroup 0 of every product reports it.
 #include "ciera.h"
+#include "mx_rules.h"
 
 namespace {
 
@@ -34,12 +35,8 @@ typedef uint32_t u32x2v __attribute__((ext_vector_type(2)));
 
 constexpr uint32_t kMxBlock = 32u;
 constexpr uint32_t kMxThreads = 256u;
-constexpr uint64_t kMxMaxRows = 1ull << 31;
-constexpr uint64_t kMxMaxCols = 1ull << 21;
 constexpr uint64_t kMxMaxLd = 1ull << 22;
-constexpr uint32_t kMxMaxGroups = 4096u;
 constexpr uint64_t kMxMostThreads = 0xFFFFFFFFu;  // of a launch
-constexpr uint64_t kMxWsHead = 512u;  // control block, then the one status word
 
 __host__ __device__ constexpr uint64_t mx_pitch(uint64_t cols) { return (cols + 127u) & ~uint64_t(127); }
 // Bytes of the value section; the scales start there.
@@ -473,8 +470,6 @@ __device__ __forceinline__ void mx_pairs(const uint32_t (&q)[kBits / 2], u32x4v 
   even = __builtin_bit_cast(v8bf, e);
   odd = __builtin_bit_cast(v8bf, o);
 }
-
-enum MxOp { kMxMatmul = 0, kMxDx = 1, kMxWgrad = 2, kMxMatmul8 = 3 };
 
 // Loads from global memory straight into LDS: lane i's 16 (or 4) bytes at
 // base + off land at lds + 16 i (4 i).  No register holds them, so they stay
@@ -1125,13 +1120,8 @@ __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_
 //             sums are added in wave order; for calls with too few rows to
 //             fill the chip otherwise.
 // 64 rows on 42 of 64 groups of 1,024 x 2,048: 13.3 us for 47 MB, 3.5 TB/s;
-// one row, n = k = 2,048: 6.9 us, a launch.  Its time grows with the outputs,
-// the tiles' does not until they fill the chip: taken below kMxFewOutputs (16
-// rows, n = 2,048: 7.9 against 12.5 us; 32 rows: 9.6 against 12.5; 64 rows: 16.5
-// against 12.6; 8 rows, n = 16,384: 12.7 against 12.9; 64 groups, n = 1,024, 64
-// rows: 15.2 against 17.7, 512 rows: 25 against 18).
+// one row, n = k = 2,048: 6.9 us, a launch.
 constexpr uint32_t kMxFewThreads = 512u;
-constexpr uint64_t kMxFewOutputs = 1u << 17;  // outputs (all tokens' n) below which it is taken
 
 // Eight values of x, c a multiple of 8: as loaded (mx8: the values, then the
 // scale byte), and as BF16.  Behind the contraction's end: zeros.
@@ -1364,24 +1354,6 @@ ciera_status mx_decode_impl(const void* d_q, uint64_t q_bytes, uint64_t rows, ui
   return launch_status();
 }
 
-constexpr uint32_t kMxCus = 256u;
-constexpr uint32_t kMxDxParts = 8u;
-uint32_t mx_wgrad_parts(uint64_t tokens, uint64_t n, uint64_t k, uint64_t groups);
-
-uint64_t mx_ws_size(uint64_t tokens, uint64_t n, uint64_t k, uint64_t groups) {
-  if (tokens > kMxMaxRows - 1u || !n || !k || n > kMxMaxCols || k > kMxMaxCols || !groups || groups > kMxMaxGroups ||
-      groups * n > kMxMaxRows)
-    return 0u;
-  // Sized for every smaller number of tokens too, some of which dx takes in
-  // more parts: as parts * tiles <= kMxCus and tokens < 64 tiles / columns'
-  // tiles, the parts' rows stay below 64 kMxCus / columns' tiles.
-  const uint64_t wgrad = mx_wgrad_parts(tokens, n, k, groups), cols = cdiv(k, 128u);
-  const uint64_t sums = wgrad > 1u ? wgrad * groups * n * k : 0u;
-  uint64_t rows = n >= 512u && cols <= kMxCus / 2u ? 64u * kMxCus / cols : 0u;
-  if (rows > kMxDxParts * tokens) rows = kMxDxParts * tokens;
-  return kMxWsHead + (sums > rows * k ? sums : rows * k) * 4u;
-}
-
 // The checks every product makes, and the arguments they share.
 ciera_status mx_product(MxArgs& p, const void* d_w, uint64_t w_bytes, void* d_out, uint64_t ldo, uint64_t out_cols,
                         uint32_t out_f32, uint64_t tokens, uint64_t n, uint64_t k, uint32_t groups,
@@ -1417,24 +1389,13 @@ ciera_status mx_product(MxArgs& p, const void* d_w, uint64_t w_bytes, void* d_ou
   return CIERA_OK;
 }
 
-// Token tiles of bm rows that the groups can need between them.
-uint64_t mx_token_tiles(uint64_t tokens, uint64_t groups, uint32_t bm) {
-  return tokens / bm + (groups < tokens ? groups : tokens);
-}
-uint64_t mx_token_tiles(const MxArgs& p, uint32_t bm) {
-  return p.offsets ? mx_token_tiles(p.tokens, p.groups, bm) : cdiv(p.tokens, bm);
-}
-
-// What the rules below go by: tiles of 128 x 256 that the output would make,
-// and the rows a group has on average.
-uint64_t mx_tiles(const MxArgs& p, uint64_t cols) { return cdiv(p.tokens, 128u) * cdiv(cols, 256u); }
-uint32_t mx_rows_each(const MxArgs& p) { return p.tokens / p.groups; }
+MxSizes mx_sizes(const MxArgs& p) { return {p.tokens, p.n, p.k, p.groups, p.offsets != nullptr}; }
 
 template <int kOp, uint32_t kBM, uint32_t kBN, uint32_t kBC, uint32_t kWM, uint32_t kWN, uint32_t kStages, uint32_t kPerCu>
 ciera_status mx_gemm_as(const MxArgs& p, hipStream_t stream) {
   constexpr bool kRowsB = kOp == kMxMatmul || kOp == kMxMatmul8;
   const uint64_t ntiles = cdiv(kRowsB ? p.n : p.k, kBN);
-  uint64_t grid = mx_token_tiles(p, kBM) * ntiles;
+  uint64_t grid = mx_token_tiles(mx_sizes(p), kBM) * ntiles;
   if (kOp == kMxWgrad) {
     grid = cdiv(p.n, kBM) * ntiles;
     if (p.groups > 1u) grid = cdiv(grid, 8u) * 8u;
@@ -1446,47 +1407,37 @@ ciera_status mx_gemm_as(const MxArgs& p, hipStream_t stream) {
 }
 template <uint32_t kBM, uint32_t kBN, uint32_t kWM, uint32_t kWN, uint32_t kStages, uint32_t kPerCu>
 ciera_status mx_gemm8_as(const MxArgs& p, hipStream_t stream) {
-  const uint64_t grid = mx_token_tiles(p, kBM) * cdiv(p.n, kBN);
+  const uint64_t grid = mx_token_tiles(mx_sizes(p), kBM) * cdiv(p.n, kBN);
   if (grid * (kWM * kWN * 64u) > kMxMostThreads) return CIERA_ERR_ARG;
   launch(k_mx_gemm8<kBM, kBN, kWM, kWN, kStages, kPerCu>, dim3(uint32_t(grid)), dim3(kWM * kWN * 64u), stream, p);
   return launch_status();
 }
 
-// The tile shapes.  Small outputs want many small tiles, so that every CU has
-// work; large ones want large tiles, which read less; and a group's last tile
-// is half empty, so tiles stay below the rows a group has.  Both sides of each
-// rule, in us (rows of one group with n = k = 2,048; "8 g", "64 g": rows of so
-// many groups together with n = 1,024, k = 2,048):
-//   matmul  32 or 64 rows: 1,024: 18.0, 18.7; 2,048: 34, 25; 2,000 in 64 g: 25, 27.5; 5,000 in 64 g: 47, 40.
-//           64 or 128 rows: 3,000: 32, 34; 4,096: 46, 37; 6,000 in 64 g: 43, 46; 8,192 in 64 g: 55, 48.
-//           128 rows, 128 or 256 columns: 4,001: 37, 41; 8,192: 72, 69; 32,768: 265, 252.
-//           x in mx8, BF16 result (the scaled instructions), 32 or 64 rows: 2,048: 21, 16; 2,000 in 64 g: 17, 23;
-//           6,000 in 64 g: 32, 30; 64 or 128 rows: 3,000: 24, 24; 8,192: 56, 44; 6,000 in 64 g: 30, 34.
-//   dx      64 x 128 or 64 x 256: 512: 23, 29; 2,048: 34, 33; 64 in 64 g: 27, 22; 4,000 in 64 g: 40, 32.
-//           32 or 64 rows of 256: 999 in 66 g with n = 1,408: 27, 31; 500 in 64 g: 18, 22; 3,000: 30, 31; 4,000: 36, 33.
-//           64 or 128 rows: 4,096: 49, 47; 8,192: 79, 73; 32,768: 277, 258; 8,192 in 8 g: 50, 52; 32,768 in 64 g: 167, 170.
 template <int kOp>
-ciera_status mx_gemm(const MxArgs& p, hipStream_t stream) {
+ciera_status mx_gemm(const MxArgs& p, MxKernel kernel, hipStream_t stream) {
   if constexpr (kOp == kMxDx) {
-    if (mx_rows_each(p) >= 1024u && mx_tiles(p, p.k) >= 2u * kMxCus)
-      return mx_gemm_as<kOp, 128u, 256u, 64u, 1u, 4u, 3u, 2u>(p, stream);
-    if (mx_token_tiles(p, 64u) * cdiv(p.k, 128u) <= 2u * kMxCus) return mx_gemm_as<kOp, 64u, 128u, 64u, 2u, 2u, 3u, 2u>(p, stream);
-    if (mx_rows_each(p) <= 48u) return mx_gemm_as<kOp, 32u, 256u, 64u, 1u, 4u, 2u, 4u>(p, stream);
-    return mx_gemm_as<kOp, 64u, 256u, 64u, 1u, 4u, 2u, 3u>(p, stream);
+    switch (kernel) {
+      case kMx128x256: return mx_gemm_as<kOp, 128u, 256u, 64u, 1u, 4u, 3u, 2u>(p, stream);
+      case kMx64x128: return mx_gemm_as<kOp, 64u, 128u, 64u, 2u, 2u, 3u, 2u>(p, stream);
+      case kMx32x256: return mx_gemm_as<kOp, 32u, 256u, 64u, 1u, 4u, 2u, 4u>(p, stream);
+      default: return mx_gemm_as<kOp, 64u, 256u, 64u, 1u, 4u, 2u, 3u>(p, stream);
+    }
   } else {
-    const uint64_t tiles = mx_tiles(p, p.n);
-    if (mx_rows_each(p) > 64u && tiles >= 2u * kMxCus) return mx_gemm_as<kOp, 128u, 256u, 64u, 2u, 2u, 3u, 2u>(p, stream);
-    if (mx_rows_each(p) > 64u && tiles > 3u * kMxCus / 4u) return mx_gemm_as<kOp, 128u, 128u, 64u, 2u, 2u, 2u, 3u>(p, stream);
     if constexpr (kOp == kMxMatmul)
-      if (mx_rows_each(p) <= 48u || tiles <= kMxCus / 4u) return mx_gemm_as<kOp, 32u, 128u, 64u, 1u, 4u, 3u, 2u>(p, stream);
-    return mx_gemm_as<kOp, 64u, 128u, 64u, 1u, 4u, 3u, 2u>(p, stream);
+      if (kernel == kMx32x128) return mx_gemm_as<kOp, 32u, 128u, 64u, 1u, 4u, 3u, 2u>(p, stream);
+    switch (kernel) {
+      case kMx128x256: return mx_gemm_as<kOp, 128u, 256u, 64u, 2u, 2u, 3u, 2u>(p, stream);
+      case kMx128x128: return mx_gemm_as<kOp, 128u, 128u, 64u, 2u, 2u, 2u, 3u>(p, stream);
+      default: return mx_gemm_as<kOp, 64u, 128u, 64u, 1u, 4u, 3u, 2u>(p, stream);
+    }
   }
 }
 ciera_status mx_gemm8(const MxArgs& p, hipStream_t stream) {
-  const uint64_t tiles = mx_tiles(p, p.n);
-  if (mx_rows_each(p) > 64u && tiles > 3u * kMxCus / 4u) return mx_gemm8_as<128u, 256u, 2u, 2u, 2u, 2u>(p, stream);
-  if (mx_rows_each(p) > 48u && tiles > kMxCus / 4u) return mx_gemm8_as<64u, 128u, 1u, 4u, 2u, 4u>(p, stream);
-  return mx_gemm8_as<32u, 128u, 1u, 4u, 3u, 2u>(p, stream);
+  switch (mx_scaled_kernel(mx_sizes(p))) {
+    case kMx128x256: return mx_gemm8_as<128u, 256u, 2u, 2u, 2u, 2u>(p, stream);
+    case kMx64x128: return mx_gemm8_as<64u, 128u, 1u, 4u, 2u, 4u>(p, stream);
+    default: return mx_gemm8_as<32u, 128u, 1u, 4u, 3u, 2u>(p, stream);
+  }
 }
 
 template <bool kMx8>
@@ -1497,39 +1448,17 @@ ciera_status mx_matmul_impl(MxArgs& p, hipStream_t stream, bool scaled = false) 
     return launch_status();
   }
   if (kMx8 && scaled) return mx_gemm8(p, stream);
-  if (uint64_t(p.tokens) * p.n < kMxFewOutputs) {
-    // 128 rows a workgroup once that gives every other CU one (one token,
-    // k = 2,048: n = 8,192: 9.0 against 8.2 us, 16,384: 8.8 against 11.0)
-    const uint64_t live = p.groups < p.tokens ? p.groups : p.tokens;
-    if (cdiv(p.n, 128u) * live >= kMxCus / 2u)
+  const MxKernel kernel = mx_matmul_kernel(mx_sizes(p), kMx8);
+  if (kernel == kMxFew128 || kernel == kMxFew16) {
+    if (kernel == kMxFew128)
       launch(k_mx_few<kMx8, 1u>, dim3(uint32_t(cdiv(p.n, 128u)), p.groups), dim3(kMxFewThreads), stream, p);
     else
       launch(k_mx_few<kMx8, 8u>, dim3(uint32_t(cdiv(p.n, 16u)), p.groups), dim3(kMxFewThreads), stream, p);
     return launch_status();
   }
-  return mx_gemm<kMx8 ? kMxMatmul8 : kMxMatmul>(p, stream);
+  return mx_gemm<kMx8 ? kMxMatmul8 : kMxMatmul>(p, kernel, stream);
 }
 
-// wgrad: where the tiles would leave CUs idle, each group's tokens go in up to
-// eight parts, at least 512 rows each on average, whose FP32 sums k_mx_join
-// adds in order (n = k = 2,048, FP32: 8,192 rows 95 against 174 us in one
-// part, 2,048 rows 43 against 52; 1,024 rows in parts of 256: 36 against 30 in
-// one).
-uint32_t mx_wgrad_parts(uint64_t tokens, uint64_t n, uint64_t k, uint64_t groups) {
-  const uint64_t tiles = cdiv(n, 256u) * cdiv(k, 128u) * groups;
-  uint64_t parts = 2u * kMxCus / tiles;
-  if (parts > tokens / groups / 512u) parts = tokens / groups / 512u;
-  return parts < 1u ? 1u : parts > 8u ? 8u : uint32_t(parts);
-}
-// dx: where even its smallest tiles leave CUs without a workgroup, n goes in up
-// to eight parts of at least 256, joined likewise (n = k = 2,048: 40 rows 14.5
-// against 23.0 us in one part, 256 rows 16.2 against 23.3).
-uint32_t mx_dx_parts(uint64_t tokens, uint64_t n, uint64_t k, uint64_t groups) {
-  const uint64_t tiles = mx_token_tiles(tokens, groups, 64u) * cdiv(k, 128u);
-  uint64_t parts = tiles ? kMxCus / tiles : 1u;
-  if (parts > n / 256u) parts = n / 256u;
-  return parts < 1u ? 1u : parts > kMxDxParts ? kMxDxParts : uint32_t(parts);
-}
 ciera_status mx_dx_impl(MxArgs p, hipStream_t stream) {
   (void)hipGetLastError();
   if (p.tokens == 0u) {
@@ -1537,12 +1466,13 @@ ciera_status mx_dx_impl(MxArgs p, hipStream_t stream) {
     return launch_status();
   }
   p.parts = mx_dx_parts(p.tokens, p.n, p.k, p.groups);
-  if (p.parts == 1u) return mx_gemm<kMxDx>(p, stream);
+  const MxKernel kernel = mx_dx_kernel(mx_sizes(p));
+  if (p.parts == 1u) return mx_gemm<kMxDx>(p, kernel, stream);
   MxArgs sums = p;
   sums.out = reinterpret_cast<uint8_t*>(p.ctrl) + kMxWsHead;
   sums.ldo = p.k;
   sums.out_f32 = 1u;
-  const ciera_status st = mx_gemm<kMxDx>(sums, stream);
+  const ciera_status st = mx_gemm<kMxDx>(sums, kernel, stream);
   if (st != CIERA_OK) return st;
   launch(k_mx_join_rows, dim3(p.tokens), dim3(kMxThreads), stream, p, static_cast<const float*>(sums.out));
   return launch_status();
