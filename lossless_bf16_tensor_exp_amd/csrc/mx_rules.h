@@ -115,7 +115,8 @@ inline uint64_t mx_rows_each(const MxSizes& s) { return s.tokens / s.groups; }
 // groups together with n = 1,024, k = 2,048):
 //   32 or 64 rows: 1,024: 18.0, 18.7; 2,048: 34, 25; 2,000 in 64 g: 25, 27.5; 5,000 in 64 g: 47, 40.
 //   64 or 128 rows: 3,000: 32, 34; 4,096: 46, 37; 6,000 in 64 g: 43, 46; 8,192 in 64 g: 55, 48.
-//   128 rows, 128 or 256 columns: 4,001: 37, 41; 8,192: 72, 69; 32,768: 265, 252.
+//   128 rows, 128 or 256 columns: 4,001: 37, 41; 8,192: 72, 69; 32,768: 265, 252; in 64 g: 154, 150.
+//     x in mx8: 8,192 with n = 4,096, k = 8,192: 455, 430; 32,768: 227, 230; in 64 g: 138, 142; 16,384 in 8 g, n = 2,048: 126, 138.
 constexpr uint64_t kMxFewOutputs = 1u << 17;  // most outputs (all tokens' n) that k_mx_few is taken for
 
 inline MxKernel mx_matmul_kernel(const MxSizes& s, bool mx8) {
@@ -126,7 +127,7 @@ inline MxKernel mx_matmul_kernel(const MxSizes& s, bool mx8) {
     const uint32_t most = s.groups == 1u ? (mx8 ? 64u : 48u) : form == kMxFew16 ? (mx8 ? 32u : 24u) : mx8 ? 8u : 6u;
     if (rows <= most) return form;
   }
-  if (rows > 64u && tiles >= 2u * kMxCus) return kMx128x256;
+  if (rows > 64u && tiles >= 2u * kMxCus && !(mx8 && s.groups > 1u)) return kMx128x256;
   if (rows > 64u && tiles > 3u * kMxCus / 4u) return kMx128x128;
   if (!mx8 && (rows <= 48u || tiles <= kMxCus / 4u)) return kMx32x128;
   return kMx64x128;
@@ -145,9 +146,10 @@ inline MxKernel mx_scaled_kernel(const MxSizes& s) {
 // The tile of dx = dy W, likewise:
 //   64 x 128 or 64 x 256: 512: 23, 29; 2,048: 34, 33; 64 in 64 g: 27, 22; 4,000 in 64 g: 40, 32.
 //   32 or 64 rows of 256: 999 in 66 g with n = 1,408: 27, 31; 500 in 64 g: 18, 22; 3,000: 30, 31; 4,000: 36, 33.
-//   64 or 128 rows: 4,096: 49, 47; 8,192: 79, 73; 32,768: 277, 258; 8,192 in 8 g: 50, 52; 32,768 in 64 g: 167, 170.
+//   64 or 128 rows: 4,096: 40, 41; 8,192: 70, 62; 32,768: 260, 245; 16,384 in 4 g: 80, 85; 8,192 in 8 g, n = 512: 29, 33;
+//     32,768 in 64 g: 167, 170; with n = 2,048: 8,192 in 2 g: 84, 93; 32,768 in 4 g: 272, 264.
 inline MxKernel mx_dx_kernel(const MxSizes& s) {
-  if (mx_rows_each(s) >= 1024u && mx_tiles(s, s.k) >= 2u * kMxCus) return kMx128x256;
+  if (mx_rows_each(s) >= 1024u && mx_tiles(s, s.k) >= (s.groups > 1u ? 8u : 2u) * kMxCus) return kMx128x256;
   if (mx_token_tiles(s, 64u) * mx_cdiv(s.k, 128u) <= 2u * kMxCus) return kMx64x128;
   return mx_rows_each(s) <= 48u ? kMx32x256 : kMx64x256;
 }

@@ -33,3 +33,21 @@ def test_no_workgroup_walks_many_rows(op, groups):
 ])
 def test_few_rows_or_tiles(op, tokens, n, groups, want):
     assert kernel(op, tokens, n, 2048, groups) == want
+
+
+@pytest.mark.parametrize("op,tokens,n,k,groups,want", [
+    # dx: 128 rows for one group of many; groups, whose last tiles are part empty, from four times as many tiles on
+    ("dx", 4096, 2048, 2048, 1, "64x256"), ("dx", 8192, 2048, 2048, 1, "128x256"), ("dx", 8192, 512, 2048, 1, "128x256"),
+    ("dx", 8192, 2048, 2048, 2, "64x256"), ("dx", 8192, 1024, 2048, 8, "64x256"), ("dx", 8192, 512, 4096, 4, "64x256"),
+    ("dx", 16384, 2048, 2048, 8, "64x256"), ("dx", 32768, 1024, 2048, 64, "64x256"), ("dx", 32768, 2048, 2048, 4, "128x256"),
+    ("dx", 65536, 1024, 2048, 16, "128x256"),
+    # and the smaller ones
+    ("dx", 512, 2048, 2048, 1, "64x128"), ("dx", 2048, 2048, 2048, 1, "64x128"), ("dx", 999, 1408, 2048, 66, "32x256"),
+    ("dx", 3000, 1024, 2048, 64, "32x256"), ("dx", 4000, 1024, 2048, 64, "64x256"),
+    # x in mx8: groups take 128 columns
+    ("mx8", 32768, 1024, 2048, 64, "128x128"), ("mx8", 16384, 2048, 2048, 8, "128x128"), ("mx8", 8192, 4096, 8192, 1, "128x256"),
+    ("mx8", 32768, 2048, 2048, 1, "128x256"), ("bf16", 32768, 1024, 2048, 64, "128x256"), ("bf16", 8192, 1024, 2048, 8, "128x128"),
+    ("mx8", 4000, 1024, 2048, 64, "64x128"), ("bf16", 4001, 2048, 2048, 1, "128x128"),
+])
+def test_tile_of_many_rows(op, tokens, n, k, groups, want):
+    assert kernel(op, tokens, n, k, groups) == want
