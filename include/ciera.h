@@ -430,9 +430,15 @@ ciera_status ciera_encode_ex(const void* d_x, uint64_t n, uint32_t B, uint8_t* d
  * Sizes: rows <= 2^31; cols, n, k <= 2^21; groups <= 4096; groups * n <= 2^31;
  * row strides (ld*, in values) from the number of columns to 2^22.  BF16 and
  * FP32 matrices need the alignment of their type only, and rows may start
- * anywhere; encoded matrices and the workspace are 16-byte aligned.  A call
- * that would need 2^32 threads (matrices of 2^36 values and more) is
- * CIERA_ERR_ARG.
+ * anywhere; encoded matrices and the workspace are 16-byte aligned.  A kernel
+ * has less than 2^32 threads; a call that would need more is CIERA_ERR_ARG:
+ *   encode      rows * cols above 2^36 - 4,096, cols rounded up to 128
+ *   decode      the same with cols rounded up to 8
+ *   y and dx    (tokens / 32 + groups + 1) * ceil(columns / 128) of 2^24 and
+ *               more may be refused (groups that have rows end in a part of a
+ *               tile each); what is below that is not
+ *   dW          groups * (ceil(n / 256) * ceil(k / 128) rounded up to 8) of
+ *               2^24 and more
  *
  * Groups: the products take `groups` weight matrices of n x k at once, encoded
  * as one matrix of groups * n rows.  Rows d_offsets[g] .. d_offsets[g + 1] - 1

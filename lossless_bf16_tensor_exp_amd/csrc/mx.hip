@@ -34,9 +34,7 @@ typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2v __attribute__((ext_vector_type(2)));
 
 constexpr uint32_t kMxBlock = 32u;
-constexpr uint32_t kMxThreads = 256u;
 constexpr uint64_t kMxMaxLd = 1ull << 22;
-constexpr uint64_t kMxMostThreads = 0xFFFFFFFFu;  // of a launch
 
 __host__ __device__ constexpr uint64_t mx_pitch(uint64_t cols) { return (cols + 127u) & ~uint64_t(127); }
 // Bytes of the value section; the scales start there.
@@ -90,8 +88,6 @@ __device__ __forceinline__ u32x4v mx_part8(const uint16_t* src, uint32_t have) {
 // of 145 (mx8) and 106 instead of 130 (mx4), 6.5 and 6.4 TB/s; of 16,384 x
 // 2,048 in mx8 36 us, 5.6 TB/s.
 // ---------------------------------------------------------------------------
-constexpr uint32_t kMxUnits = 2u;
-
 struct MxUnitAt {
   uint64_t row;
   uint32_t col;
@@ -1329,9 +1325,8 @@ ciera_status mx_encode_impl(const void* d_x, uint64_t rows, uint64_t cols, uint6
   if (st == CIERA_OK) st = mx_encoded(d_q, q_bytes, rows, cols, kBits, CIERA_ERR_CAPACITY);
   if (st != CIERA_OK || !rows || !cols) return st;
   const uint64_t at = mx_scales_at(rows, cols, kBits);
-  const uint64_t units = rows * (mx_pitch(cols) / 8u);
-  const uint64_t grid = cdiv(units, kMxThreads * kMxUnits);
-  if (grid * kMxThreads > kMxMostThreads) return CIERA_ERR_ARG;
+  const uint64_t grid = mx_unit_groups(rows, mx_pitch(cols));
+  if (grid > kMxMostGroups) return CIERA_ERR_ARG;
   uint8_t* q = static_cast<uint8_t*>(d_q);
   (void)hipGetLastError();
   launch(k_mx_encode<kBits>, dim3(uint32_t(grid)), dim3(kMxThreads), stream, static_cast<const uint16_t*>(d_x), rows,
@@ -1345,8 +1340,8 @@ ciera_status mx_decode_impl(const void* d_q, uint64_t q_bytes, uint64_t rows, ui
   ciera_status st = mx_matrix(d_y, rows, cols, ld, 2u);
   if (st == CIERA_OK) st = mx_encoded(d_q, q_bytes, rows, cols, kBits, CIERA_ERR_FORMAT);
   if (st != CIERA_OK || !rows || !cols) return st;
-  const uint64_t grid = cdiv(rows * cdiv(cols, 8u), kMxThreads * kMxUnits);
-  if (grid * kMxThreads > kMxMostThreads) return CIERA_ERR_ARG;
+  const uint64_t grid = mx_unit_groups(rows, cols);
+  if (grid > kMxMostGroups) return CIERA_ERR_ARG;
   const uint8_t* q = static_cast<const uint8_t*>(d_q);
   (void)hipGetLastError();
   launch(k_mx_decode<kBits>, dim3(uint32_t(grid)), dim3(kMxThreads), stream, q, q + mx_scales_at(rows, cols, kBits),
@@ -1393,22 +1388,17 @@ MxSizes mx_sizes(const MxArgs& p) { return {p.tokens, p.n, p.k, p.groups, p.offs
 
 template <int kOp, uint32_t kBM, uint32_t kBN, uint32_t kBC, uint32_t kWM, uint32_t kWN, uint32_t kStages, uint32_t kPerCu>
 ciera_status mx_gemm_as(const MxArgs& p, hipStream_t stream) {
-  constexpr bool kRowsB = kOp == kMxMatmul || kOp == kMxMatmul8;
-  const uint64_t ntiles = cdiv(kRowsB ? p.n : p.k, kBN);
-  uint64_t grid = mx_token_tiles(mx_sizes(p), kBM) * ntiles;
-  if (kOp == kMxWgrad) {
-    grid = cdiv(p.n, kBM) * ntiles;
-    if (p.groups > 1u) grid = cdiv(grid, 8u) * 8u;
-    grid *= p.groups * p.parts;
-  }
-  if (grid * (kWM * kWN * 64u) > kMxMostThreads) return CIERA_ERR_ARG;
+  static_assert(kWM * kWN * 64u == kMxThreads, "what kMxMostGroups counts with");
+  const uint64_t grid = mx_tile_groups(kOp, kBM, kBN, mx_sizes(p), p.parts);
+  if (grid > kMxMostGroups) return CIERA_ERR_ARG;
   launch(k_mx_gemm<kOp, kBM, kBN, kBC, kWM, kWN, kStages, kPerCu>, dim3(uint32_t(grid), kOp == kMxDx ? p.parts : 1u), dim3(kWM * kWN * 64u), stream, p);
   return launch_status();
 }
 template <uint32_t kBM, uint32_t kBN, uint32_t kWM, uint32_t kWN, uint32_t kStages, uint32_t kPerCu>
 ciera_status mx_gemm8_as(const MxArgs& p, hipStream_t stream) {
-  const uint64_t grid = mx_token_tiles(mx_sizes(p), kBM) * cdiv(p.n, kBN);
-  if (grid * (kWM * kWN * 64u) > kMxMostThreads) return CIERA_ERR_ARG;
+  static_assert(kWM * kWN * 64u == kMxThreads, "what kMxMostGroups counts with");
+  const uint64_t grid = mx_tile_groups(kMxMatmul8, kBM, kBN, mx_sizes(p), 1u);
+  if (grid > kMxMostGroups) return CIERA_ERR_ARG;
   launch(k_mx_gemm8<kBM, kBN, kWM, kWN, kStages, kPerCu>, dim3(uint32_t(grid)), dim3(kWM * kWN * 64u), stream, p);
   return launch_status();
 }

@@ -13,6 +13,9 @@ constexpr uint32_t kMxMaxGroups = 4096u;
 constexpr uint64_t kMxWsHead = 512u;  // of the workspace: control block, then the one status word
 constexpr uint32_t kMxCus = 256u;
 constexpr uint32_t kMxDxParts = 8u;
+constexpr uint32_t kMxThreads = 256u;                            // of a workgroup (k_mx_few: 512)
+constexpr uint64_t kMxMostGroups = 0xFFFFFFFFu / kMxThreads;     // of a launch: below 2^32 threads
+constexpr uint32_t kMxUnits = 2u;                                // units of 8 values that a thread encodes or decodes
 
 enum MxOp { kMxMatmul = 0, kMxDx = 1, kMxWgrad = 2, kMxMatmul8 = 3 };
 
@@ -44,6 +47,20 @@ inline uint64_t mx_token_tiles(uint64_t tokens, uint64_t groups, uint32_t bm) {
 }
 inline uint64_t mx_token_tiles(const MxSizes& s, uint32_t bm) {
   return s.offsets ? mx_token_tiles(s.tokens, s.groups, bm) : mx_cdiv(s.tokens, bm);
+}
+
+// Workgroups of an encode (cols: the padded ones) or a decode.
+inline uint64_t mx_unit_groups(uint64_t rows, uint64_t cols) {
+  return mx_cdiv(rows * mx_cdiv(cols, 8u), kMxThreads * kMxUnits);
+}
+// Workgroups of a product in tiles of bm x bn (dx's parts are the grid's second
+// dimension).  k_mx_few's stay far below the limit: cdiv(n, 16) <= 2^13.
+inline uint64_t mx_tile_groups(int op, uint32_t bm, uint32_t bn, const MxSizes& s, uint32_t parts) {
+  if (op == kMxWgrad) {
+    const uint64_t tiles = mx_cdiv(s.n, bm) * mx_cdiv(s.k, bn);
+    return (s.groups > 1u ? mx_cdiv(tiles, 8u) * 8u : tiles) * s.groups * parts;  // groups: an eighth of them an XCD
+  }
+  return mx_token_tiles(s, bm) * mx_cdiv(op == kMxDx ? s.k : s.n, bn);
 }
 
 // wgrad: where the tiles would leave CUs idle, each group's tokens go in up to

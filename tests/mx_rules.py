@@ -13,6 +13,10 @@ int matmul_kernel(uint64_t t, uint64_t n, uint64_t k, uint32_t g, int o, int mx8
 int scaled_kernel(uint64_t t, uint64_t n, uint64_t k, uint32_t g, int o) { return mx_scaled_kernel({t, n, k, g, o != 0}); }
 int dx_kernel(uint64_t t, uint64_t n, uint64_t k, uint32_t g, int o) { return mx_dx_kernel({t, n, k, g, o != 0}); }
 uint32_t dx_parts(uint64_t t, uint64_t n, uint64_t k, uint32_t g) { return mx_dx_parts(t, n, k, g); }
+uint64_t unit_groups(uint64_t rows, uint64_t cols) { return mx_unit_groups(rows, cols); }
+uint64_t tile_groups(int op, uint32_t bm, uint32_t bn, uint64_t t, uint64_t n, uint64_t k, uint32_t g, int o, uint32_t parts) {
+  return mx_tile_groups(op, bm, bn, {t, n, k, g, o != 0}, parts);
+}
 uint32_t wgrad_parts(uint64_t t, uint64_t n, uint64_t k, uint32_t g) { return mx_wgrad_parts(t, n, k, g); }
 }
 """
@@ -35,6 +39,8 @@ def rules():
                                 ("dx_parts", [], u32), ("wgrad_parts", [], u32)):
             f = getattr(_rules, name)
             f.argtypes, f.restype = [u64, u64, u64, u32] + tail, res
+        _rules.unit_groups.argtypes, _rules.unit_groups.restype = [u64, u64], u64
+        _rules.tile_groups.argtypes, _rules.tile_groups.restype = [i32, u32, u32, u64, u64, u64, u32, i32, u32], u64
     return _rules
 
 

@@ -1,9 +1,15 @@
 """Which kernel the microscaled products choose (no GPU: mx_rules.h compiled
 for the host).  Each listed choice is the faster of the two that were timed, or
 within a tenth of it."""
+import ctypes
+import os
+import random
+
 import pytest
 
-from mx_rules import kernel
+from mx_rules import kernel, rules
+
+torch = pytest.importorskip("torch")
 
 
 @pytest.mark.parametrize("op", ["bf16", "mx8"])
@@ -51,3 +57,68 @@ def test_few_rows_or_tiles(op, tokens, n, groups, want):
 ])
 def test_tile_of_many_rows(op, tokens, n, k, groups, want):
     assert kernel(op, tokens, n, k, groups) == want
+
+
+MOST = (2 ** 32 - 1) // 256  # workgroups of 256 threads
+
+
+def workgroups(op, tokens, n, k, groups):
+    r = rules()
+    if op == "wgrad":
+        return r.tile_groups(2, 256, 128, tokens, n, k, groups, 1, r.wgrad_parts(tokens, n, k, groups))
+    name = kernel(op, tokens, n, k, groups)
+    if name.startswith("few"):
+        return 2 * -(-n // (128 if name == "few128" else 16))  # of 512 threads; the groups are another dimension
+    return r.tile_groups({"bf16": 0, "dx": 1, "mx8": 3, "scaled": 3}[op], *map(int, name.split("x")), tokens, n, k, groups,
+                         int(groups > 1), 1)
+
+
+def test_what_the_contract_allows_is_launched():
+    """Every kernel of sizes that the header does not except has less than 2^32 threads."""
+    gen = random.Random(1)
+    top = {"bf16": 0, "mx8": 0, "scaled": 0, "dx": 0, "wgrad": 0}
+    for _ in range(20000):
+        groups = min(4096, int(2 ** gen.uniform(0, 12.01)))
+        tokens = int(2 ** gen.uniform(0, 31)) - 1
+        n = min(2 ** 21, 2 ** 31 // groups, int(2 ** gen.uniform(0, 21.01)))
+        k = min(2 ** 21, int(2 ** gen.uniform(0, 21.01)))
+        for op in top:
+            if op == "wgrad":
+                count = groups * (-(-(-(-n // 256) * -(-k // 128)) // 8) * 8)
+            else:
+                count = (tokens // 32 + groups + 1) * -(-(k if op == "dx" else n) // 128)
+            if count < 2 ** 24:
+                need = workgroups(op, tokens, n, k, groups)
+                assert need <= MOST, (op, tokens, n, k, groups)
+                top[op] = max(top[op], need)
+    assert all(t > MOST // 16 for t in top.values()), top  # the search came near the border
+    for rows, cols, ok in ((2 ** 29 - 32, 128, True), (2 ** 29 - 31, 128, False), (2 ** 31, 24, True), (2 ** 31, 25, False),
+                           (2 ** 31, 32, False), (2 ** 15 - 1, 2 ** 21, True), (2 ** 15, 2 ** 21, False)):
+        assert (rules().unit_groups(rows, cols) <= MOST) == ok, (rows, cols)
+        assert ok == (rows * (-(-cols // 8) * 8) <= 2 ** 36 - 4096)
+
+
+def test_what_needs_more_threads_is_refused_before_a_launch():
+    import lossless_bf16_tensor_exp_amd as ciera
+    if not os.path.exists(ciera.library_path()):
+        from lossless_bf16_tensor_exp_amd import build
+        build.build()
+    from lossless_bf16_tensor_exp_amd import mx as calls
+    lib, p, big = calls._lib(), ctypes.c_void_p(1 << 16), 1 << 62
+    for enc in (lib.mx8_encode, lib.mx4_encode):
+        assert enc(p, 2 ** 29, 1, 1, p, big, None) == 1
+        assert enc(p, 2 ** 15, 2 ** 21, 2 ** 21, p, big, None) == 1
+    for dec in (lib.mx8_decode, lib.mx4_decode):
+        assert dec(p, big, 2 ** 31, 32, p, 32, None) == 1
+    g, n = 4096, 2 ** 19
+    for f in (lib.mx4_matmul, lib.mx4_matmul_mx8):
+        ldx = big if f is lib.mx4_matmul_mx8 else 64
+        assert workgroups("mx8" if f is lib.mx4_matmul_mx8 else "bf16", 4096, n, 64, g) > MOST
+        assert f(p, ldx, p, big, p, n, 0, 4096, n, 64, g, p, p, big, None) == 1
+    assert workgroups("scaled", 4096, n, 64, g) > MOST
+    assert lib.mx4_matmul_mx8(p, big, p, big, p, n, 4, 4096, n, 64, g, p, p, big, None) == 1
+    n = 2 ** 21
+    assert workgroups("dx", 4096, 64, n, g) > MOST
+    assert lib.mx4_matmul_dx(p, 64, p, big, p, n, 0, 4096, 64, n, g, p, p, big, None) == 1
+    assert workgroups("wgrad", 64, 1, 2 ** 21, g) > MOST
+    assert lib.mx8_wgrad(p, 1, p, big, p, 0, 0, 64, 1, 2 ** 21, g, p, p, big, None) == 1
