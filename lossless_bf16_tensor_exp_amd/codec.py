@@ -108,7 +108,8 @@ class MxLinear:
 
     ``keep`` and the calls that read the checkpoint share one buffer, so one
     layer's forward and backward belong to one stream, or are ordered by the
-    caller.  ``backward`` takes the offsets its ``keep`` had."""
+    caller.  ``backward`` takes the offsets its ``keep`` had.  Autograd records
+    none of this; ``backward`` is the caller's to call."""
 
     def __init__(self, tokens: int, n: int, k: int, groups: int = 1, device="cuda", scaled: bool = False):
         self.tokens, self.n, self.k, self.groups, self.scaled = tokens, n, k, groups, scaled

@@ -496,7 +496,12 @@ __device__ __forceinline__ uint32_t mx_lds(const void* at) {
 // Staged tiles.  A row of R bytes is kept as 16-byte chunks; chunk c of row r
 // sits at c ^ mx_turn<R>(r), so that lanes which read (or write) one chunk of
 // 16 consecutive rows touch all 64 banks once.  The loads above apply it by
-// choosing which chunk a lane fetches.
+// choosing which chunk a lane fetches.  Two kinds of reads go without: W's rows
+// of 32 bytes in the matmuls, whose chunks of 16 rows lie in half the banks
+// (turned by r / 8: no change in time), and the scales, 16 bytes a row, whose
+// words of 32 rows lie in 16 banks.  They are all of the conflicts that the
+// counters show there (a third to a half of the LDS's busy cycles, which are 22
+// to 34 % of the time; none with both kinds of reads made free of them).
 template <uint32_t kRow>
 __device__ __forceinline__ uint32_t mx_turn(uint32_t r) {
   static_assert(kRow == 64u || kRow == 128u, "4 or 8 chunks");

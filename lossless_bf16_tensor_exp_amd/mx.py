@@ -20,6 +20,10 @@ numbers on the device) the rows offsets[g] .. offsets[g+1] - 1 belong to
 group g and ``w`` holds groups matrices one behind the other; ``dw`` is then
 (groups, n, k).  Every tensor is on one device; a call made while another
 device is current runs on the tensors' own, on that device's current stream.
+
+Nothing here is recorded by autograd: the calls write through addresses, an
+input's ``requires_grad`` has no effect, and the gradients are the calls
+``mx4_matmul_dx`` and ``mx8_wgrad``, made by the caller.
 """
 from __future__ import annotations
 

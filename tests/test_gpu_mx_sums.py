@@ -158,3 +158,21 @@ def test_layer_chooses():
             c.mx4_matmul_mx8(layer.xq, k, layer.w, want, layer.ws, scaled=scaled and dtype == torch.bfloat16)
             assert torch.equal(y, want)
             assert layer.error() == 0
+
+
+def test_values_past_bf16():
+    """6 * 2^127 is infinite as BF16, and in the sums of BF16 products; the scaled instructions take it as it is."""
+    say("mx8 values past BF16")
+    c = lib()
+    k = 96
+    for tokens, n in ((2, 40), (300, 200)):
+        x, w = torch.zeros(tokens, k, dtype=torch.bfloat16), torch.zeros(n, k, dtype=torch.bfloat16)
+        x[:, 40], w[:, 40] = 2.0 ** -30, 6.0
+        xq, wq = mx.encode(8, x), mx.encode(4, w)
+        wq[mx.sections(4, n, k)[1]:] = 254
+        ws = torch.empty(c.mx_workspace_size(tokens, n, k, 1), dtype=torch.uint8, device="cuda")
+        y = torch.zeros(tokens, n, dtype=torch.bfloat16, device="cuda")
+        c.mx4_matmul_mx8(xq.cuda(), k, wq.cuda(), y, ws)
+        assert (y == float("inf")).all()
+        c.mx4_matmul_mx8(xq.cuda(), k, wq.cuda(), y, ws, scaled=True)
+        assert (y == 6 * 2.0 ** 97).all()
