@@ -492,7 +492,8 @@ ciera_status mx4_decode(const void* d_q, uint64_t q_bytes, uint64_t rows, uint64
  *   d_w   in   groups * n x k mx4 of w_bytes
  *   d_y   out  tokens x n, row stride ldy: BF16 (y_f32 = 0) or FP32 (1);
  *              mx4_matmul_mx8 also takes CIERA_MX_SCALED: BF16, by the scaled
- *              matrix instructions (faster, and less exact as said above)
+ *              matrix instructions (faster on many rows, and less exact as said
+ *              above)
  *   d_ws  tmp  ws_bytes >= mx_workspace_size(tokens, n, k, groups)
  * An encoded matrix below its size is CIERA_ERR_FORMAT. */
 ciera_status mx4_matmul(const void* d_x, uint64_t ldx, const void* d_w, uint64_t w_bytes, void* d_y, uint64_t ldy,

@@ -104,7 +104,7 @@ class MxLinear:
     numbers) the experts of a mixture-of-experts layer, whose groups (n, k)
     matrices lie one behind the other.  Takes up to ``tokens`` rows a call.
     With ``scaled``, ``keep`` takes a BF16 y from the scaled matrix
-    instructions (``mx4_matmul_mx8``: faster, less exact than an FP32 sum).
+    instructions (``mx4_matmul_mx8``: faster on many rows, less exact than FP32).
 
     ``keep`` and the calls that read the checkpoint share one buffer, so one
     layer's forward and backward belong to one stream, or are ordered by the

@@ -134,3 +134,16 @@ def test_long_contraction_of_real_values(op, name, shape):
         check(case, "matmul", case.xq64, y.cpu(), torch.zeros_like(y, device="cpu"), False, cut=True)
         return
     run_all(case, torch.bfloat16, exact=False, ops=({"bf16": "matmul"}.get(op, op),))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(2000, 64, 40), (8000, 16, 33), (100, 16, 1), (200, 3, 7), (70, 1, 5), (65, 1, 1), (129, 130, 2),
+                                   (500, 48, 8, 3, 1, 2), (4000, 5, 6, 40), (49, 48, 2048), (90, 1, 2048, 2, 3, 3)])
+@pytest.mark.parametrize("ldw", [(0, 0), (3, 1)])
+def test_tall_and_narrow(shape, ldw):
+    """Many rows of few columns, contractions down to one value."""
+    require_gpu()
+    say(f"mx tall and narrow {shape} ld+{ldw}")
+    case = Case(sum(shape), *shape)
+    for out in (torch.float32, torch.bfloat16):
+        run_all(case, out, exact=True, ldw=ldw)
