@@ -951,12 +951,12 @@ __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_
 // its largest product, which is more than an FP32 sum may lose: it is the
 // caller's choice, and k_mx_gemm and k_mx_few compute what is not asked for
 // here.  On activations with a few loud channels the result moved by 1/7 of a
-// BF16 rounding at the most.  128 contraction values (four
-// blocks) a step, the ring and the tile as in k_mx_gemm; the padded pitch
-// leaves no partial step.  8,192 rows in 64 groups, n = 1,024, k = 2,048: 35
-// us, to FP32 by k_mx_gemm 51; 32,768 rows: 84 us, 1.64 PFLOP/s, bound by what
-// its loads keep in flight, 43 KB a CU.  A row's four scale bytes of a step are
-// read as one word (byte by byte: 87 us).
+// BF16 rounding at the most.  128 contraction values (four blocks) a step, the
+// ring and the tile as in k_mx_gemm; the padded pitch leaves no partial step.
+// 8,192 rows in 64 groups, n = 1,024, k = 2,048: 35 us (k_mx_gemm 51); 32,768
+// rows: 84 us (141), 1.64 PFLOP/s, bound by what its loads keep in flight, 43
+// KB a CU.  A row's four scale bytes of a step are read as one word (byte by
+// byte: 87 us).
 template <uint32_t kBM, uint32_t kBN, uint32_t kWM, uint32_t kWN, uint32_t kStages, uint32_t kPerCu>
 __global__ __launch_bounds__(kWM * kWN * 64u, kWM* kWN / 4u * kPerCu) void k_mx_gemm8(MxArgs p) {
   constexpr uint32_t kW = kWM * kWN;
