@@ -116,12 +116,13 @@ inline uint64_t mx_rows_each(const MxSizes& s) { return s.tokens / s.groups; }
 // 9.0 against 8.2 us, 16,384: 8.8 against 11.0), else 16.
 // And its workgroups take a group's rows 16 at a time, one pass after the
 // other, while the tiles take them at once, so it is for few rows a group, on
-// average; the larger groups of uneven ones then need two passes, or three of
-// the shorter ones of the split form (n = 256, k = 2,048 and 8,192):
+// average; the larger groups of uneven ones (the more groups, the larger) then
+// need two passes, or three of the shorter ones of the split form (n = 256, k =
+// 2,048 and 8,192):
 //   one group, split: 32 rows: 9.1, 24 against 11.8, 40; 48: 12.5, 35 against 11.8, 40; 64: 16.2, 45 against 11.8,
 //     40; 2,000 rows of n = 64: 470, 1,434 against 12.3, 41.  x in mx8, k = 2,048: 64: 14.7 against 16.8; 128: 27, 17.
-//   groups, split: 96 rows in 4: 12.4, 32 against 12.7, 40; 128 in 4: 14.6, 43 against 12.7, 40; 512 in 16: 18.8, 54
-//     against 13.0, 41.  mx8: 512 in 16: 16.1 against 17.8; 1,024 in 16: 25, 18.
+//   groups, split: 96 rows in 4: 12.4, 32 against 12.7, 40; 128 in 4: 14.6, 43 against 12.7, 40; 256 in 16: 12.2, 33
+//     against 12.8, 41; 384 in 16: 14.8, 42 against 12.9, 41.  mx8: 512 in 16: 16.1 against 17.8; 1,024 in 16: 25, 18.
 //   groups, 128 rows a workgroup: 256 rows in 64: 10.8, 35 against 13.0, 41; 384 in 64: 15.5, 52 against 13.1, 46;
 //     n = 1,024: 96 in 16: 11.4, 37 against 13.4, 41; 128 in 16: 17.7, 60 against 13.4, 41.  mx8: 512 in 64: 16.1, 17.4.
 //
@@ -141,7 +142,9 @@ inline MxKernel mx_matmul_kernel(const MxSizes& s, bool mx8) {
   if (s.tokens * s.n <= kMxFewOutputs) {
     const uint64_t live = s.groups < s.tokens ? s.groups : s.tokens;
     const MxKernel form = mx_cdiv(s.n, 128u) * live >= kMxCus / 2u ? kMxFew128 : kMxFew16;
-    const uint32_t most = s.groups == 1u ? (mx8 ? 64u : 48u) : form == kMxFew16 ? (mx8 ? 32u : 24u) : mx8 ? 8u : 6u;
+    uint32_t most = mx8 ? 64u : 48u;
+    if (s.groups > 1u && form == kMxFew16) most = mx8 ? 32u : s.groups <= 8u ? 24u : 16u;
+    if (s.groups > 1u && form == kMxFew128) most = mx8 ? 8u : s.groups <= 32u ? 6u : 5u;
     if (rows <= most) return form;
   }
   if (rows > 64u && tiles >= 2u * kMxCus && !(mx8 && s.groups > 1u)) return kMx128x256;

@@ -33,7 +33,8 @@ def test_no_workgroup_walks_many_rows(op, groups):
     ("bf16", 64, 1024, 64, "few128"), ("bf16", 128, 1024, 64, "few128"), ("bf16", 256, 512, 64, "few128"),
     ("bf16", 64, 2048, 16, "few128"), ("bf16", 512, 256, 64, "32x128"), ("bf16", 128, 1024, 16, "32x128"),
     ("bf16", 512, 1024, 64, "32x128"), ("bf16", 96, 48, 4, "few16"), ("bf16", 128, 256, 16, "few16"),
-    ("bf16", 512, 48, 64, "few16"), ("bf16", 2000, 48, 64, "32x128"), ("bf16", 512, 48, 16, "32x128"),
+    ("bf16", 96, 1024, 16, "few128"), ("bf16", 384, 256, 64, "32x128"), ("bf16", 256, 256, 16, "few16"),
+    ("bf16", 384, 256, 16, "32x128"), ("bf16", 128, 256, 4, "32x128"), ("bf16", 512, 48, 64, "few16"), ("bf16", 2000, 48, 64, "32x128"), ("bf16", 512, 48, 16, "32x128"),
     ("mx8", 256, 512, 64, "few128"), ("mx8", 512, 256, 64, "few128"), ("mx8", 512, 128, 16, "few16"),
     ("mx8", 1024, 48, 16, "64x128"), ("mx8", 256, 1024, 16, "64x128"),
 ])
