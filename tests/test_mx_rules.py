@@ -123,3 +123,17 @@ def test_what_needs_more_threads_is_refused_before_a_launch():
     assert lib.mx4_matmul_dx(p, 64, p, big, p, n, 0, 4096, 64, n, g, p, p, big, None) == 1
     assert workgroups("wgrad", 64, 1, 2 ** 21, g) > MOST
     assert lib.mx8_wgrad(p, 1, p, big, p, 0, 0, 64, 1, 2 ** 21, g, p, p, big, None) == 1
+
+
+def test_only_the_mx8_product_takes_the_scaled_instructions():
+    from lossless_bf16_tensor_exp_amd import mx as calls
+    lib, p, big = calls._lib(), ctypes.c_void_p(1 << 16), 1 << 40
+    assert lib.mx4_matmul(p, 64, p, big, p, 48, 4, 8, 48, 64, 1, None, p, big, None) == 1
+    assert lib.mx4_matmul_dx(p, 48, p, big, p, 64, 4, 8, 48, 64, 1, None, p, big, None) == 1
+    assert lib.mx8_wgrad(p, 48, p, big, p, 4, 0, 8, 48, 64, 1, None, p, big, None) == 1
+    for kind in (2, 3, 5, 8):
+        assert lib.mx4_matmul_mx8(p, big, p, big, p, 48, kind, 8, 48, 64, 1, None, p, big, None) == 1
+    for bad in (dict(q=None), dict(y=None), dict(ws=100), dict(wb=100), dict(qb=100)):  # as for the others
+        a = dict(dict(q=p, qb=big, wb=big, y=p, ws=big), **bad)
+        st = lib.mx4_matmul_mx8(a["q"], a["qb"], p, a["wb"], a["y"], 48, 4, 8, 48, 64, 1, None, p, a["ws"], None)
+        assert st == {"q": 1, "y": 1, "ws": 3, "wb": 5, "qb": 5}[next(iter(bad))]
