@@ -516,6 +516,136 @@ ciera_status mx8_wgrad(const void* d_dy, uint64_t lddy, const void* d_xq, uint64
                        uint32_t dw_f32, uint32_t accumulate, uint64_t tokens, uint64_t n, uint64_t k, uint32_t groups,
                        const int64_t* d_offsets, void* d_ws, uint64_t ws_bytes, hipStream_t stream);
 
+/* What stands around the products of a layer: the norm before them, the
+ * adapters beside them, and for the experts of a mixture-of-experts layer the
+ * rows brought to them and back.  All of it takes BF16 matrices as the products
+ * do (any row stride, any alignment of the type), is asynchronous, launches
+ * only kernels, and gives equal bits for equal calls.  Sizes, where not said
+ * otherwise: rows, tokens <= 2^31, cols, n, k <= 2^21, row strides to 2^22; a
+ * launch that would need 2^32 threads or more is CIERA_ERR_ARG.  Products and
+ * sums are FP32, and every output is rounded once. */
+
+/* rms_norm: h = x + residual, s = 1 / sqrt(mean(h^2) + eps), y = h s w.
+ *   d_x         in   rows x cols BF16, row stride ldx; cols <= 32768
+ *   d_residual  in   the same, or null: then h is x
+ *   d_w         in   cols BF16
+ *   eps         > 0
+ *   d_h         out  h in BF16, or null (and null without a residual); may be
+ *                    d_x or d_residual with its stride
+ *   d_y         out  y in BF16, or null; may be d_x with its stride
+ *   d_yq        out  mx8_encode's bytes of that y, yq_bytes >= its encoded size
+ *                    (else CIERA_ERR_CAPACITY), or null; one of d_y and d_yq is
+ *                    given
+ *   d_rstd      out  s of every row, FP32, or null
+ * The norm is that of h rounded to BF16.  A row whose sum of squares passes
+ * FP32's range, or holds an infinity, has s = 0: y is NaN at the infinities and
+ * 0 elsewhere.  A NaN makes the whole row NaN.
+ *
+ * rms_norm_backward, with u = h s and g = dy w:  dx = s (g - u mean(g u)) + dh,
+ * dw = sum over the rows of dy u.
+ *   d_dy        in   rows x cols BF16, the gradient of y
+ *   d_h         in   h (x without a residual), and d_rstd as rms_norm left it
+ *   d_dh        in   the gradient that h has from elsewhere (the residual's
+ *                    way past the layer), or null
+ *   d_dx        out  the gradient of x, and of the residual, in BF16, or null
+ *                    (and then no d_dh); may be d_dy or d_dh with its stride
+ *   d_dw        out  cols BF16 (dw_f32 = 0) or FP32 (1), or null; accumulate =
+ *                    1 adds to it (one rounding of the sum)
+ *   d_ws        tmp  ws_bytes >= rms_norm_workspace_size(rows, cols); needed
+ *                    for d_dw only; holds no status for ciera_read_error */
+ciera_status rms_norm(const void* d_x, uint64_t ldx, const void* d_residual, uint64_t ldr, const void* d_w, float eps,
+                      void* d_h, uint64_t ldh, void* d_y, uint64_t ldy, void* d_yq, uint64_t yq_bytes, float* d_rstd,
+                      uint64_t rows, uint64_t cols, hipStream_t stream);
+/* One size serves every smaller number of rows; 0 when a size is out of range. */
+uint64_t rms_norm_workspace_size(uint64_t rows, uint64_t cols);
+ciera_status rms_norm_backward(const void* d_dy, uint64_t lddy, const void* d_h, uint64_t ldh, const void* d_w,
+                               const float* d_rstd, const void* d_dh, uint64_t lddh, void* d_dx, uint64_t lddx,
+                               void* d_dw, uint32_t dw_f32, uint32_t accumulate, uint64_t rows, uint64_t cols,
+                               void* d_ws, uint64_t ws_bytes, hipStream_t stream);
+
+/* Rows of tokens to their experts and back.  A token has `choices` (1 .. 64)
+ * entries, each of them an expert or none; tokens * choices < 2^31, experts <=
+ * 4096.
+ *
+ * expert_sort: the entries sorted by expert, those of one expert in their order.
+ *   d_ids      in   tokens x choices, int32 (ids_i64 = 0) or int64 (1): an
+ *                   expert, or -1 for none.  Any other number goes with none,
+ *                   and ciera_read_error(d_ws) then reports CIERA_ERR_ARG.
+ *   d_offsets  out  experts + 1 int64: expert e's rows are d_offsets[e] ..
+ *                   d_offsets[e + 1] - 1, as the mx products take them
+ *   d_place    out  tokens x choices int32: the row of each entry, -1 for one
+ *                   of no expert
+ *   d_order    out  tokens * choices int32, or null: the entry of each row, and
+ *                   behind the last expert's rows the entries of none
+ *   d_ws       tmp  ws_bytes >= expert_workspace_size(tokens, choices, experts)
+ *
+ * expert_dispatch: x[t] to row d_place[t][j] for every entry with one.
+ *   d_x     in   tokens x cols BF16
+ *   d_out   out  rows x cols BF16, or null
+ *   d_outq  out  the mx8 matrix of rows x cols, or null: every row's bytes as
+ *                mx8_encode makes them; outq_bytes as there
+ * Rows that no entry has keep their bytes; places of `rows` or more are left
+ * out.  An entry's place is its own: equal places make their row undefined.
+ * Its gradient is expert_combine of the rows' gradients without weights.
+ *
+ * expert_combine: out[t] = residual[t] + sum over j of weight[t][j] *
+ * rows[place[t][j]], the choices in order.
+ *   d_rows      in   rows x cols, BF16 (rows_f32 = 0) or FP32 (1)
+ *   d_weights   in   tokens x choices FP32, or null for ones
+ *   d_residual  in   tokens x cols BF16, or null for zeros
+ *   d_out       out  tokens x cols, BF16 or FP32; may be d_residual with its
+ *                    type and stride
+ * An entry without a row adds nothing, whatever its weight.
+ *
+ * expert_combine_backward: drows[place[t][j]] = weight[t][j] * dout[t], and
+ * dweights[t][j] = <dout[t], rows[place[t][j]]>, 0 for an entry without a row.
+ *   d_dout      in   tokens x cols BF16
+ *   d_drows     out  rows x cols BF16, or null; rows that no entry has keep
+ *                    their values
+ *   d_dweights  out  tokens x choices FP32, or null (d_rows is then not read)
+ * The gradient of the residual is dout. */
+uint64_t expert_workspace_size(uint64_t tokens, uint64_t choices, uint32_t experts);
+ciera_status expert_sort(const void* d_ids, uint32_t ids_i64, uint64_t tokens, uint64_t choices, uint32_t experts,
+                         int64_t* d_offsets, int32_t* d_place, int32_t* d_order, void* d_ws, uint64_t ws_bytes,
+                         hipStream_t stream);
+ciera_status expert_dispatch(const void* d_x, uint64_t ldx, const int32_t* d_place, uint64_t tokens, uint64_t choices,
+                             uint64_t cols, uint64_t rows, void* d_out, uint64_t ldo, void* d_outq, uint64_t outq_bytes,
+                             hipStream_t stream);
+ciera_status expert_combine(const void* d_rows, uint64_t ldrows, uint32_t rows_f32, uint64_t rows, const int32_t* d_place,
+                            const float* d_weights, const void* d_residual, uint64_t ldr, void* d_out, uint64_t ldo,
+                            uint32_t out_f32, uint64_t tokens, uint64_t choices, uint64_t cols, hipStream_t stream);
+ciera_status expert_combine_backward(const void* d_dout, uint64_t lddout, const void* d_rows, uint64_t ldrows,
+                                     uint32_t rows_f32, uint64_t rows, const int32_t* d_place, const float* d_weights,
+                                     void* d_drows, uint64_t lddrows, float* d_dweights, uint64_t tokens,
+                                     uint64_t choices, uint64_t cols, hipStream_t stream);
+
+/* low_rank_add: y_t = base_t + s_a B_a (A_a x_t), a the adapter of row t: the
+ * low-rank adapters of many requests beside the projection `base` that they
+ * share.  For serving: there is no gradient of it here.
+ *   d_x        in   tokens x k BF16
+ *   d_a, d_b   in   adapters x rank x k and adapters x n x rank BF16,
+ *                   contiguous; rank <= 128, adapters <= 4096
+ *   d_scales   in   adapters FP32, or null for ones
+ *   d_offsets  in   adapters + 1 int64 and
+ *   d_order    in   tokens int32: adapter a's rows are d_order[d_offsets[a]] ..
+ *                   d_order[d_offsets[a + 1] - 1], as expert_sort leaves them
+ *                   for one choice a token; null: the rows lie in that order
+ *   d_base     in   tokens x n, BF16 (base_f32 = 0) or FP32 (1), or null for
+ *                   zeros; may be d_y with its type and stride
+ *   d_y        out  tokens x n, BF16 (y_f32 = 0) or FP32 (1)
+ *   d_ws       tmp  ws_bytes >= low_rank_workspace_size(...)
+ * The rows before the first and behind the last adapter's have none: y is base
+ * there.  Offsets out of order, or past tokens: as for the mx products.  An
+ * order that names a row twice or leaves one out leaves those rows undefined;
+ * a row out of range is left out.  The inner values A_a x_t are FP32; an
+ * infinity in d_b gives NaN. */
+uint64_t low_rank_workspace_size(uint64_t tokens, uint64_t n, uint64_t k, uint64_t rank, uint32_t adapters);
+ciera_status low_rank_add(const void* d_x, uint64_t ldx, const void* d_a, const void* d_b, const float* d_scales,
+                          const int64_t* d_offsets, const int32_t* d_order, const void* d_base, uint64_t ldb,
+                          uint32_t base_f32, void* d_y, uint64_t ldy, uint32_t y_f32, uint64_t tokens, uint64_t n,
+                          uint64_t k, uint64_t rank, uint32_t adapters, void* d_ws, uint64_t ws_bytes,
+                          hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

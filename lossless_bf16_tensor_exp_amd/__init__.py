@@ -1,6 +1,7 @@
 """Lossless BF16 codec for MI355X: exponent reuse across iterations (CIERA)
 plus the sigma-windowed 3-bit exponent code (ZipCCL), in hand-written HIP; and
-matrices in 8 and 4 bits with the products of a linear layer on them.
+matrices in 8 and 4 bits with the products of a linear layer on them, and what
+stands around those products in a layer.
 
 This package is a thin binding over the C ABI in ``include/ciera.h``
 (``libciera.so``, built in-tree by ``build.py``).  Every step of the codec
@@ -33,6 +34,7 @@ Same names as the C ABI::
     ciera_set_wait_limit(polls)           (test hook: bound of the waits between workgroups)
     ciera_encode_noalloc(x, B, prev_exp, out, out_size, stream=None)   (no workspace: allocates nothing)
     mx8_* / mx4_*                         (8- and 4-bit matrices and their products: ``mx.py``)
+    rms_norm* / expert_* / low_rank_*     (what stands around those products in a layer: ``layers.py``)
 
 ``x``/``y`` are CUDA(HIP) tensors of dtype bfloat16, int16 or uint16 holding
 the BF16 patterns; ``out``/``inp``/``ws``/``prev_exp`` are uint8 tensors and
@@ -56,6 +58,8 @@ __all__ = [
     "CHUNK",
     "mx8_encoded_size", "mx4_encoded_size", "mx_workspace_size", "mx8_encode", "mx8_decode", "mx4_encode", "mx4_decode",
     "mx4_matmul", "mx4_matmul_mx8", "mx4_matmul_dx", "mx8_wgrad",
+    "rms_norm", "rms_norm_backward", "rms_norm_workspace_size", "expert_sort", "expert_workspace_size", "expert_dispatch",
+    "expert_combine", "expert_combine_backward", "low_rank_add", "low_rank_workspace_size",
 ]
 
 CHUNK = 65536
@@ -484,14 +488,18 @@ def ciera_set_wait_limit(polls: int) -> int:
 
 _MX = ("mx8_encoded_size", "mx4_encoded_size", "mx_workspace_size", "mx8_encode", "mx8_decode", "mx4_encode",
        "mx4_decode", "mx4_matmul", "mx4_matmul_mx8", "mx4_matmul_dx", "mx8_wgrad")
+_LAYERS = ("rms_norm", "rms_norm_backward", "rms_norm_workspace_size", "expert_sort", "expert_workspace_size",
+           "expert_dispatch", "expert_combine", "expert_combine_backward", "low_rank_add", "low_rank_workspace_size")
 
 
 def __getattr__(name):
-    """The microscaled matrices' calls, bound at first use: ``mx.py`` needs
-    torch, which importing this package does not load."""
-    if name in _MX:
-        from . import mx
-        for f in _MX:
-            globals()[f] = getattr(mx, f)
+    """The microscaled matrices' calls and those around them, bound at first
+    use: ``mx.py`` and ``layers.py`` need torch, which importing this package
+    does not load."""
+    if name in _MX or name in _LAYERS:
+        from . import layers, mx
+        for module, names in ((mx, _MX), (layers, _LAYERS)):
+            for f in names:
+                globals()[f] = getattr(module, f)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,525 @@
+// experts.hip -- rows of tokens brought to their experts and back, gfx950.
+//
+// ids[t][j] is the expert of token t's j-th choice, an entry; -1 for none.
+//   sort      offsets[e] = entries of experts below e; place[i] = offsets[e_i]
+//             + entries of e_i before i (-1 without expert); order[place[i]] =
+//             i, and behind the last expert's the entries without one, in order
+//   dispatch  out[place[t][j]] = x[t], in BF16 or mx8
+//   combine   out[t] = residual[t] + sum_j w[t][j] rows[place[t][j]]
+//   backward  drows[place[t][j]] = w[t][j] dout[t];
+//             dw[t][j] = <dout[t], rows[place[t][j]]>
+// Entries without a row add nothing and are not read; rows of no entry are not
+// written.  Sums are FP32 and in the order of the choices (dw: an order that
+// depends on the sizes only); every output is rounded once.
+#include "ciera.h"
+
+namespace {
+
+constexpr uint32_t kMaxChoices = 64u;
+constexpr uint64_t kMaxEntries = (1ull << 31) - 1u;
+constexpr uint32_t kSortWords = 16u * 1024u + 64u;  // of LDS: a count for each wave and bin
+constexpr uint32_t kSortBlocks = 256u;
+
+// A sort goes in up to kSortBlocks blocks of at least 4,096 entries, fewer for
+// many experts: every block reads the counts of all of them.
+uint32_t sort_blocks(uint64_t entries, uint32_t experts) {
+  uint64_t b = entries / 4096u;
+  const uint64_t most = 65536u / (experts + 1u);
+  if (b > most) b = most;
+  if (b > kSortBlocks) b = kSortBlocks;
+  return b < 1u ? 1u : uint32_t(b);
+}
+constexpr uint32_t sort_waves(uint32_t experts) { return experts < 1024u ? 16u : 4u; }
+
+struct SortArgs {
+  const void* ids;
+  int64_t* offsets;
+  int32_t* place;
+  int32_t* order;
+  uint32_t* counts;  // blocks x (experts + 1), then a word a block: whether it met a bad id
+  Ctrl* ctrl;
+  uint32_t* status;
+  uint32_t entries, experts, blocks, per;  // per: entries a block
+};
+
+// Bin of entry i: its expert, or `experts` for none.  A number that is neither
+// goes with none and is reported.
+template <bool kWide>
+__device__ __forceinline__ uint32_t sort_bin(const SortArgs& p, uint32_t i, bool& bad) {
+  int64_t e;
+  if constexpr (kWide) e = static_cast<const int64_t*>(p.ids)[i];
+  else e = static_cast<const int32_t*>(p.ids)[i];
+  const bool in = e >= 0 && e < int64_t(p.experts);
+  bad = bad || (!in && e != -1);
+  return in ? uint32_t(e) : p.experts;
+}
+
+// Entries of each bin among this wave's, into its row of counts.
+template <bool kWide>
+__device__ __forceinline__ bool sort_count(const SortArgs& p, uint32_t from, uint32_t to, uint32_t* count) {
+  bool bad = false;
+  for (uint32_t i = from + (threadIdx.x & 63u); i < to; i += 64u) atomicAdd(count + sort_bin<kWide>(p, i, bad), 1u);
+  return bad;
+}
+
+// This wave's entries: its share of the block's, in order.
+__device__ __forceinline__ void sort_share(const SortArgs& p, uint32_t& from, uint32_t& to) {
+  const uint32_t waves = blockDim.x >> 6, wave = threadIdx.x >> 6;
+  const uint32_t lo = min(blockIdx.x * p.per, p.entries), hi = min(lo + p.per, p.entries);
+  const uint32_t each = ((hi - lo + waves - 1u) / waves + 63u) & ~63u;
+  from = min(lo + wave * each, hi);
+  to = min(from + each, hi);
+}
+
+template <bool kWide>
+__global__ __launch_bounds__(1024) void k_sort_count(SortArgs p) {
+  __shared__ uint32_t count[4097];
+  __shared__ uint32_t any;
+  const uint32_t bins = p.experts + 1u;
+  for (uint32_t b = threadIdx.x; b < bins; b += blockDim.x) count[b] = 0u;
+  if (threadIdx.x == 0u) any = 0u;
+  __syncthreads();
+  uint32_t from, to;
+  sort_share(p, from, to);
+  if (sort_count<kWide>(p, from, to, count)) any = 1u;
+  __syncthreads();
+  for (uint32_t b = threadIdx.x; b < bins; b += blockDim.x) p.counts[uint64_t(blockIdx.x) * bins + b] = count[b];
+  if (threadIdx.x == 0u) p.counts[uint64_t(p.blocks) * bins + blockIdx.x] = any;
+}
+
+// Each wave takes a stretch of the entries and counts it; the counts become
+// the places where the wave's entries of each bin begin; then the wave goes
+// through its stretch again, 64 entries a step.  Lanes of one bin find each
+// other with a ballot for each bit of the bin's number; the first of them
+// draws their places.
+template <bool kWide>
+__global__ __launch_bounds__(1024) void k_expert_sort(SortArgs p) {
+  __shared__ uint32_t count[kSortWords];
+  __shared__ uint32_t sums[16];
+  __shared__ uint32_t any;
+  const uint32_t tid = threadIdx.x, threads = blockDim.x, lane = tid & 63u, wave = tid >> 6, waves = threads >> 6;
+  const uint32_t bins = p.experts + 1u;
+  for (uint32_t i = tid; i < waves * bins; i += threads) count[i] = 0u;
+  if (tid == 0u) any = 0u;
+  __syncthreads();
+  uint32_t from, to;
+  sort_share(p, from, to);
+  uint32_t* mine = count + wave * bins;
+  const bool bad = sort_count<kWide>(p, from, to, mine);
+  if (p.blocks == 1u && bad) any = 1u;
+  if (p.blocks > 1u && blockIdx.x == 0u)
+    for (uint32_t b = tid; b < p.blocks; b += threads)
+      if (p.counts[uint64_t(p.blocks) * bins + b]) any = 1u;
+  __syncthreads();
+  uint32_t before = 0u;  // entries of the bins so far
+  for (uint32_t c = 0; c < bins; c += threads) {
+    const uint32_t b = c + tid;
+    uint32_t all = 0u, earlier = 0u;
+    if (b < bins) {
+      if (p.blocks == 1u) {
+        for (uint32_t w = 0; w < waves; w++) all += count[w * bins + b];
+      } else {
+#pragma unroll 8
+        for (uint32_t k = 0; k < p.blocks; k++) {
+          const uint32_t n = p.counts[uint64_t(k) * bins + b];
+          all += n;
+          if (k < blockIdx.x) earlier += n;
+        }
+      }
+    }
+    const uint32_t sum = mx_scan(all);
+    if (lane == 63u) sums[wave] = sum;
+    __syncthreads();
+    uint32_t at = before + sum - all, total = 0u;
+    for (uint32_t w = 0; w < waves; w++) {
+      if (w < wave) at += sums[w];
+      total += sums[w];
+    }
+    before += total;
+    if (b < bins) {
+      if (blockIdx.x == 0u) p.offsets[b] = int64_t(at);  // the bin of none begins where the last expert's end
+      at += earlier;
+      for (uint32_t w = 0; w < waves; w++) {
+        const uint32_t n = count[w * bins + b];
+        count[w * bins + b] = at;
+        at += n;
+      }
+    }
+    __syncthreads();
+  }
+  const uint32_t bits = 32u - uint32_t(__clz(int(bins)));
+  for (uint32_t i0 = from; i0 < to; i0 += 64u) {
+    const uint32_t i = i0 + lane;
+    bool ignored = false;
+    const uint32_t b = i < to ? sort_bin<kWide>(p, i, ignored) : bins;
+    uint64_t same = ~0ull;
+    for (uint32_t k = 0; k < bits; k++) {
+      const uint64_t set = __ballot((b >> k) & 1u);
+      same &= ((b >> k) & 1u) ? set : ~set;
+    }
+    const uint32_t rank = uint32_t(__popcll(same & ((1ull << lane) - 1u)));
+    uint32_t first = 0u;
+    if (rank == 0u && b < bins) first = atomicAdd(mine + b, uint32_t(__popcll(same)));
+    first = uint32_t(__shfl(int(first), __ffsll((unsigned long long)same) - 1));
+    if (b < bins) {
+      const uint32_t at = first + rank;
+      p.place[i] = b < p.experts ? int32_t(at) : -1;
+      if (p.order) p.order[at] = int32_t(i);
+    }
+  }
+  if (blockIdx.x == 0u && tid == 0u) {
+    p.ctrl->n_err_slots = 1u;
+    *p.status = any ? uint32_t(CIERA_ERR_ARG) : uint32_t(CIERA_OK);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The rows.  A token takes 1 << lt threads, each a unit of 8 values or several
+// that far apart; a workgroup of 256 holds 256 >> lt tokens.
+// ---------------------------------------------------------------------------
+struct RowArgs {
+  const uint16_t* x;  // dispatch: the tokens; backward: dout
+  uint64_t ldx;
+  const void* rows;   // combine, backward: the experts' rows, BF16 or FP32
+  uint64_t ldrows;
+  const int32_t* place;
+  const float* weights;
+  const uint16_t* residual;
+  uint64_t ldr;
+  void* out;          // dispatch: rows; combine: tokens; backward: drows
+  uint64_t ldo;
+  uint8_t* q;         // dispatch: rows in mx8
+  uint8_t* qs;
+  float* dweights;
+  uint32_t out_f32, tokens, choices, cols, slots, lt;
+};
+
+// The token of this thread and its place in the token's row.  With a wave or
+// more a token its number is the same in all lanes, and is kept so.
+template <bool kWave>
+__device__ __forceinline__ uint32_t row_token(const RowArgs& p, uint32_t& t) {
+  t = threadIdx.x & ((1u << p.lt) - 1u);
+  const uint32_t sub = threadIdx.x >> p.lt;
+  return blockIdx.x * (256u >> p.lt) + (kWave ? mx_first(sub) : sub);
+}
+
+template <bool kWave>
+__global__ __launch_bounds__(256) void k_dispatch(RowArgs p) {
+  uint32_t t;
+  const uint32_t token = row_token<kWave>(p, t);
+  if (token >= p.tokens) return;
+  const uint16_t* x = p.x + uint64_t(token) * p.ldx;
+  const int32_t* place = p.place + uint64_t(token) * p.choices;
+  const uint32_t kp = uint32_t(mx_pitch(p.cols));
+  const uint32_t end = p.q ? kp : p.cols;
+  for (uint32_t col = t * 8u; col < end; col += 8u << p.lt) {
+    const u32x4v v = row_load8(x, col, p.cols);
+    u32x2v codes = {0u, 0u};
+    uint32_t sb = 0u;
+    if (p.q) {
+      u32x4v e = v;
+      sb = mx_block_scale<8>(e);
+      codes = mx8_codes(e, mx_scale(sb == 255u ? 127u : sb));
+    }
+    for (uint32_t j = 0; j < p.choices; j++) {
+      const uint32_t at = uint32_t(place[j]);
+      if (at >= p.slots) continue;
+      if (p.out) row_store8(static_cast<uint16_t*>(p.out) + uint64_t(at) * p.ldo, col, p.cols, v);
+      if (p.q) {
+        *reinterpret_cast<u32x2v*>(p.q + uint64_t(at) * kp + col) = codes;
+        if ((t & 3u) == 0u) p.qs[uint64_t(at) * (kp / 32u) + col / 32u] = uint8_t(sb);
+      }
+    }
+  }
+}
+
+// Eight FP32 values from column `col` of a BF16 or FP32 row, zeros behind it.
+template <bool kF32>
+__device__ __forceinline__ void row_values8(const void* rows, uint64_t at, uint32_t col, uint32_t cols, float (&v)[8]) {
+  if constexpr (kF32) {
+    const float* r = static_cast<const float*>(rows) + at;
+    if (col + 8u <= cols) {
+      const v4f a = *reinterpret_cast<const v4fa4*>(r + col), b = *reinterpret_cast<const v4fa4*>(r + col + 4u);
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        v[i] = a[i];
+        v[4 + i] = b[i];
+      }
+    } else {
+#pragma unroll
+      for (uint32_t i = 0; i < 8u; i++) v[i] = col + i < cols ? r[col + i] : 0.0f;
+    }
+  } else {
+    const u32x4v w = row_load8(static_cast<const uint16_t*>(rows) + at, col, cols);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      v[2 * i] = bf_lo(w[i]);
+      v[2 * i + 1] = bf_hi(w[i]);
+    }
+  }
+}
+
+template <bool kWave, bool kF32>
+__global__ __launch_bounds__(256) void k_combine(RowArgs p) {
+  uint32_t t;
+  const uint32_t token = row_token<kWave>(p, t);
+  if (token >= p.tokens) return;
+  const int32_t* place = p.place + uint64_t(token) * p.choices;
+  const float* weights = p.weights ? p.weights + uint64_t(token) * p.choices : nullptr;
+  for (uint32_t col = t * 8u; col < p.cols; col += 8u << p.lt) {
+    float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if (p.residual) row_values8<false>(p.residual, uint64_t(token) * p.ldr, col, p.cols, sum);
+    for (uint32_t j0 = 0; j0 < p.choices; j0 += 4u) {
+      float v[4][8], w[4];
+      bool has[4];
+#pragma unroll
+      for (uint32_t i = 0; i < 4u; i++) {
+        const uint32_t at = j0 + i < p.choices ? uint32_t(place[j0 + i]) : ~0u;
+        has[i] = at < p.slots;
+        w[i] = has[i] && weights ? weights[j0 + i] : 1.0f;
+        if (has[i]) row_values8<kF32>(p.rows, uint64_t(at) * p.ldrows, col, p.cols, v[i]);
+      }
+#pragma unroll
+      for (uint32_t i = 0; i < 4u; i++)
+        if (has[i])
+#pragma unroll
+          for (int c = 0; c < 8; c++) sum[c] = fmaf(w[i], v[i][c], sum[c]);
+    }
+    const uint64_t to = uint64_t(token) * p.ldo;
+    if (p.out_f32) {
+      float* o = static_cast<float*>(p.out) + to + col;
+      if (col + 8u <= p.cols) {
+        *reinterpret_cast<v4fa4*>(o) = v4f{sum[0], sum[1], sum[2], sum[3]};
+        *reinterpret_cast<v4fa4*>(o + 4) = v4f{sum[4], sum[5], sum[6], sum[7]};
+      } else {
+#pragma unroll
+        for (uint32_t i = 0; i < 7u; i++)
+          if (col + i < p.cols) o[i] = sum[i];
+      }
+    } else {
+      row_store8(static_cast<uint16_t*>(p.out) + to, col, p.cols,
+                 u32x4v{mx_bf16x2(sum[0], sum[1]), mx_bf16x2(sum[2], sum[3]), mx_bf16x2(sum[4], sum[5]), mx_bf16x2(sum[6], sum[7])});
+    }
+  }
+}
+
+// The choices go four at a time, dout read again for each four.
+template <bool kWave, bool kF32>
+__global__ __launch_bounds__(256) void k_combine_back(RowArgs p) {
+  __shared__ float part[2][4][4];
+  uint32_t t;
+  const uint32_t token = row_token<kWave>(p, t);
+  const bool live = token < p.tokens;
+  const int32_t* place = p.place + uint64_t(live ? token : 0u) * p.choices;
+  const float* weights = p.weights ? p.weights + uint64_t(live ? token : 0u) * p.choices : nullptr;
+  const uint16_t* x = p.x + uint64_t(live ? token : 0u) * p.ldx;
+  const uint32_t span = min(1u << p.lt, 64u);
+  for (uint32_t j0 = 0, turn = 0; j0 < p.choices; j0 += 4u, turn ^= 1u) {
+    uint32_t at[4];
+    float w[4], dot[4];
+#pragma unroll
+    for (uint32_t i = 0; i < 4u; i++) {
+      at[i] = live && j0 + i < p.choices ? uint32_t(place[j0 + i]) : ~0u;
+      w[i] = at[i] < p.slots && weights ? weights[j0 + i] : 1.0f;
+      dot[i] = 0.0f;
+    }
+    for (uint32_t col = t * 8u; live && col < p.cols; col += 8u << p.lt) {
+      float d[8];
+      row_values8<false>(x, 0u, col, p.cols, d);
+      if (p.dweights) {
+        float v[4][8];
+#pragma unroll
+        for (uint32_t i = 0; i < 4u; i++)
+          if (at[i] < p.slots) row_values8<kF32>(p.rows, uint64_t(at[i]) * p.ldrows, col, p.cols, v[i]);
+#pragma unroll
+        for (uint32_t i = 0; i < 4u; i++)
+          if (at[i] < p.slots)
+#pragma unroll
+            for (int c = 0; c < 8; c++) dot[i] = fmaf(d[c], v[i][c], dot[i]);
+      }
+      if (p.out) {
+#pragma unroll
+        for (uint32_t i = 0; i < 4u; i++)
+          if (at[i] < p.slots)
+            row_store8(static_cast<uint16_t*>(p.out) + uint64_t(at[i]) * p.ldo, col, p.cols,
+                       u32x4v{mx_bf16x2(w[i] * d[0], w[i] * d[1]), mx_bf16x2(w[i] * d[2], w[i] * d[3]),
+                              mx_bf16x2(w[i] * d[4], w[i] * d[5]), mx_bf16x2(w[i] * d[6], w[i] * d[7])});
+      }
+    }
+    if (!p.dweights) continue;
+#pragma unroll
+    for (uint32_t i = 0; i < 4u; i++)
+      for (uint32_t s = span >> 1; s > 0u; s >>= 1) dot[i] += __shfl_xor(dot[i], int(s));
+    if (p.lt > 6u) {
+      if ((threadIdx.x & 63u) == 0u)
+#pragma unroll
+        for (uint32_t i = 0; i < 4u; i++) part[turn][threadIdx.x >> 6][i] = dot[i];
+      __syncthreads();
+      const uint32_t waves = 1u << (p.lt - 6u), w0 = threadIdx.x >> 6 & ~(waves - 1u);
+#pragma unroll
+      for (uint32_t i = 0; i < 4u; i++) {
+        dot[i] = 0.0f;
+        for (uint32_t k = 0; k < waves; k++) dot[i] += part[turn][w0 + k][i];
+      }
+    }
+    if (live && t == 0u)
+#pragma unroll
+      for (uint32_t i = 0; i < 4u; i++)
+        if (j0 + i < p.choices) p.dweights[uint64_t(token) * p.choices + j0 + i] = at[i] < p.slots ? dot[i] : 0.0f;
+  }
+}
+
+// log2 of the threads a token takes: a unit each, at least a block of mx8 and
+// at most a workgroup.
+uint32_t row_threads(uint64_t cols) {
+  uint32_t lt = 2u;
+  while (lt < 8u && (8ull << lt) < cols) lt++;
+  return lt;
+}
+
+ciera_status row_common(RowArgs& p, const int32_t* d_place, uint64_t tokens, uint64_t choices, uint64_t cols, uint64_t slots) {
+  if (choices == 0u || choices > kMaxChoices || tokens > kMxMaxRows || tokens * choices > kMaxEntries || slots > kMxMaxRows ||
+      cols > kMxMaxCols)
+    return CIERA_ERR_ARG;
+  if (tokens && (!d_place || (reinterpret_cast<uintptr_t>(d_place) & 3u) != 0u)) return CIERA_ERR_ARG;
+  p.place = d_place;
+  p.tokens = uint32_t(tokens);
+  p.choices = uint32_t(choices);
+  p.cols = uint32_t(cols);
+  p.slots = uint32_t(slots);
+  p.lt = row_threads(cols);
+  return cdiv(tokens, 256u >> p.lt) > kMxMostGroups ? CIERA_ERR_ARG : CIERA_OK;
+}
+dim3 row_grid(const RowArgs& p) { return dim3(uint32_t(cdiv(p.tokens, 256u >> p.lt))); }
+
+}  // namespace
+
+extern "C" {
+
+uint64_t expert_workspace_size(uint64_t tokens, uint64_t choices, uint32_t experts) {
+  if (choices == 0u || choices > kMaxChoices || tokens > kMxMaxRows || tokens * choices > kMaxEntries || experts == 0u ||
+      experts > kMxMaxGroups)
+    return 0u;
+  // any smaller number of tokens takes no more blocks
+  return align256(kMxWsHead + 4ull * sort_blocks(tokens * choices, experts) * (experts + 2u));
+}
+
+ciera_status expert_sort(const void* d_ids, uint32_t ids_i64, uint64_t tokens, uint64_t choices, uint32_t experts,
+                         int64_t* d_offsets, int32_t* d_place, int32_t* d_order, void* d_ws, uint64_t ws_bytes,
+                         hipStream_t stream) {
+  const uint64_t need = expert_workspace_size(tokens, choices, experts);
+  if (!need || ids_i64 > 1u) return CIERA_ERR_ARG;
+  ciera_status st = norm_vector(d_offsets, 8u);
+  if (st == CIERA_OK && tokens) st = norm_vector(d_ids, ids_i64 ? 8u : 4u);
+  if (st == CIERA_OK && tokens) st = norm_vector(d_place, 4u);
+  if (st == CIERA_OK && d_order) st = norm_vector(d_order, 4u);
+  if (st != CIERA_OK || !d_ws || !aligned16(d_ws)) return CIERA_ERR_ARG;
+  if (ws_bytes < need) return CIERA_ERR_WORKSPACE;
+  SortArgs p{};
+  p.ids = d_ids;
+  p.offsets = d_offsets;
+  p.place = d_place;
+  p.order = d_order;
+  p.ctrl = static_cast<Ctrl*>(d_ws);
+  p.status = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(d_ws) + sizeof(Ctrl));
+  p.counts = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(d_ws) + kMxWsHead);
+  p.entries = uint32_t(tokens * choices);
+  p.experts = experts;
+  p.blocks = sort_blocks(p.entries, experts);
+  p.per = uint32_t(cdiv(p.entries, p.blocks));
+  const dim3 block(64u * sort_waves(experts));
+  (void)hipGetLastError();
+  if (p.blocks > 1u) {
+    if (ids_i64) launch(k_sort_count<true>, dim3(p.blocks), block, stream, p);
+    else launch(k_sort_count<false>, dim3(p.blocks), block, stream, p);
+  }
+  if (ids_i64) launch(k_expert_sort<true>, dim3(p.blocks), block, stream, p);
+  else launch(k_expert_sort<false>, dim3(p.blocks), block, stream, p);
+  return launch_status();
+}
+
+ciera_status expert_dispatch(const void* d_x, uint64_t ldx, const int32_t* d_place, uint64_t tokens, uint64_t choices,
+                             uint64_t cols, uint64_t rows, void* d_out, uint64_t ldo, void* d_outq, uint64_t outq_bytes,
+                             hipStream_t stream) {
+  RowArgs p{};
+  if (!d_out && !d_outq && rows) return CIERA_ERR_ARG;
+  ciera_status st = row_common(p, d_place, tokens, choices, cols, rows);
+  if (st == CIERA_OK) st = mx_matrix(d_x, tokens, cols, ldx, 2u);
+  if (st == CIERA_OK && d_out) st = mx_matrix(d_out, rows, cols, ldo, 2u);
+  if (st == CIERA_OK && d_outq) st = mx_encoded(d_outq, outq_bytes, rows, cols, 8u, CIERA_ERR_CAPACITY);
+  if (st != CIERA_OK || !tokens || !cols || !rows) return st;
+  p.x = static_cast<const uint16_t*>(d_x);
+  p.ldx = ldx;
+  p.out = d_out;
+  p.ldo = ldo;
+  p.q = static_cast<uint8_t*>(d_outq);
+  p.qs = p.q ? p.q + mx_scales_at(rows, cols, 8u) : nullptr;
+  (void)hipGetLastError();
+  if (p.lt >= 6u) launch(k_dispatch<true>, row_grid(p), dim3(256), stream, p);
+  else launch(k_dispatch<false>, row_grid(p), dim3(256), stream, p);
+  return launch_status();
+}
+
+ciera_status expert_combine(const void* d_rows, uint64_t ldrows, uint32_t rows_f32, uint64_t rows, const int32_t* d_place,
+                            const float* d_weights, const void* d_residual, uint64_t ldr, void* d_out, uint64_t ldo,
+                            uint32_t out_f32, uint64_t tokens, uint64_t choices, uint64_t cols, hipStream_t stream) {
+  RowArgs p{};
+  if (rows_f32 > 1u || out_f32 > 1u) return CIERA_ERR_ARG;
+  ciera_status st = row_common(p, d_place, tokens, choices, cols, rows);
+  if (st == CIERA_OK) st = mx_matrix(d_rows, rows, cols, ldrows, rows_f32 ? 4u : 2u);
+  if (st == CIERA_OK) st = mx_matrix(d_out, tokens, cols, ldo, out_f32 ? 4u : 2u);
+  if (st == CIERA_OK && d_residual) st = mx_matrix(d_residual, tokens, cols, ldr, 2u);
+  if (st == CIERA_OK && d_weights) st = norm_vector(d_weights, 4u);
+  if (st != CIERA_OK || !tokens || !cols) return st;
+  p.rows = d_rows;
+  p.ldrows = ldrows;
+  p.weights = d_weights;
+  p.residual = static_cast<const uint16_t*>(d_residual);
+  p.ldr = ldr;
+  p.out = d_out;
+  p.ldo = ldo;
+  p.out_f32 = out_f32;
+  (void)hipGetLastError();
+  if (p.lt >= 6u) {
+    if (rows_f32) launch(k_combine<true, true>, row_grid(p), dim3(256), stream, p);
+    else launch(k_combine<true, false>, row_grid(p), dim3(256), stream, p);
+  } else {
+    if (rows_f32) launch(k_combine<false, true>, row_grid(p), dim3(256), stream, p);
+    else launch(k_combine<false, false>, row_grid(p), dim3(256), stream, p);
+  }
+  return launch_status();
+}
+
+ciera_status expert_combine_backward(const void* d_dout, uint64_t lddout, const void* d_rows, uint64_t ldrows,
+                                     uint32_t rows_f32, uint64_t rows, const int32_t* d_place, const float* d_weights,
+                                     void* d_drows, uint64_t lddrows, float* d_dweights, uint64_t tokens,
+                                     uint64_t choices, uint64_t cols, hipStream_t stream) {
+  RowArgs p{};
+  if (rows_f32 > 1u || (!d_drows && !d_dweights && tokens && rows)) return CIERA_ERR_ARG;
+  ciera_status st = row_common(p, d_place, tokens, choices, cols, rows);
+  if (st == CIERA_OK) st = mx_matrix(d_dout, tokens, cols, lddout, 2u);
+  if (st == CIERA_OK && d_dweights) st = mx_matrix(d_rows, rows, cols, ldrows, rows_f32 ? 4u : 2u);
+  if (st == CIERA_OK && d_dweights) st = norm_vector(d_dweights, 4u);
+  if (st == CIERA_OK && d_drows) st = mx_matrix(d_drows, rows, cols, lddrows, 2u);
+  if (st == CIERA_OK && d_weights) st = norm_vector(d_weights, 4u);
+  if (st != CIERA_OK || !tokens) return st;
+  p.x = static_cast<const uint16_t*>(d_dout);
+  p.ldx = lddout;
+  p.rows = d_rows;
+  p.ldrows = ldrows;
+  p.weights = d_weights;
+  p.out = d_drows;
+  p.ldo = lddrows;
+  p.dweights = d_dweights;
+  (void)hipGetLastError();
+  if (p.lt >= 6u) {
+    if (rows_f32) launch(k_combine_back<true, true>, row_grid(p), dim3(256), stream, p);
+    else launch(k_combine_back<true, false>, row_grid(p), dim3(256), stream, p);
+  } else {
+    if (rows_f32) launch(k_combine_back<false, true>, row_grid(p), dim3(256), stream, p);
+    else launch(k_combine_back<false, false>, row_grid(p), dim3(256), stream, p);
+  }
+  return launch_status();
+}
+
+}  // extern "C"

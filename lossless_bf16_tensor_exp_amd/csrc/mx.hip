@@ -76,6 +76,43 @@ __device__ __forceinline__ u32x4v mx_part8(const uint16_t* src, uint32_t have) {
   return w;
 }
 
+// The scale byte of a block of 32 BF16 values, eight of them in each of four
+// neighbouring lanes.  A block that holds an infinity or a NaN becomes zeros
+// with scale byte 255.
+template <int kBits>
+__device__ __forceinline__ uint32_t mx_block_scale(u32x4v& v) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const uint32_t a = v[i] & 0x7FFF7FFFu;
+    m = max(m, max(a & 0xFFFFu, a >> 16));
+  }
+  m = max(m, uint32_t(__builtin_amdgcn_mov_dpp(int(m), 0xB1, 0xF, 0xF, true)));  // lane ^ 1
+  m = max(m, uint32_t(__builtin_amdgcn_mov_dpp(int(m), 0x4E, 0xF, 0xF, true)));  // lane ^ 2
+  // 448 = 1.75 2^8, 6 = 1.5 2^2: one binade more when the significand of
+  // the largest value is above that
+  constexpr int kTopExp = kBits == 8 ? 8 : 2;
+  constexpr uint32_t kTopMan = kBits == 8 ? 96u : 64u;
+  const int e = int(m >> 7) - kTopExp + int((m & 127u) > kTopMan);
+  if (m >= 0x7F80u) {  // an infinity or a NaN in the block
+    v = u32x4v{0u, 0u, 0u, 0u};
+    return 255u;
+  }
+  return uint32_t(e < 1 ? 1 : e);
+}
+// Eight BF16 values over the scale s as e4m3 codes.
+__device__ __forceinline__ u32x2v mx8_codes(u32x4v v, float s) {
+  u32x2v out;
+#pragma unroll
+  for (int h = 0; h < 2; h++) {
+    v2s r = {0, 0};
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, mx_bf2(v[2 * h]), s, false);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, mx_bf2(v[2 * h + 1]), s, true);
+    out[h] = __builtin_bit_cast(uint32_t, r);
+  }
+  return out;
+}
+
 // ---------------------------------------------------------------------------
 // Encode and decode.  A unit is 8 values of a row (16 bytes of BF16); four
 // neighbouring lanes hold a block and find its largest magnitude with two
@@ -126,35 +163,12 @@ __global__ __launch_bounds__(kMxThreads) void k_mx_encode(const uint16_t* __rest
       const uint32_t have = at[u].row < rows && at[u].col < cols ? cols - at[u].col : 0u;
       v[u] = mx_part8(x + (have ? at[u].row * ld + at[u].col : 0u), have);
     }
-    uint32_t m = 0u;
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const uint32_t a = v[u][i] & 0x7FFF7FFFu;
-      m = max(m, max(a & 0xFFFFu, a >> 16));
-    }
-    m = max(m, uint32_t(__builtin_amdgcn_mov_dpp(int(m), 0xB1, 0xF, 0xF, true)));  // lane ^ 1
-    m = max(m, uint32_t(__builtin_amdgcn_mov_dpp(int(m), 0x4E, 0xF, 0xF, true)));  // lane ^ 2
-    // 448 = 1.75 2^8, 6 = 1.5 2^2: one binade more when the significand of
-    // the largest value is above that
-    constexpr int kTopExp = kBits == 8 ? 8 : 2;
-    constexpr uint32_t kTopMan = kBits == 8 ? 96u : 64u;
-    const int e = int(m >> 7) - kTopExp + int((m & 127u) > kTopMan);
-    const bool bad = m >= 0x7F80u;  // an infinity or a NaN in the block
-    const uint32_t sb = bad ? 255u : uint32_t(e < 1 ? 1 : e);
-    const float s = mx_scale(bad ? 127u : sb);
-    if (bad) v[u] = u32x4v{0u, 0u, 0u, 0u};
+    const uint32_t sb = mx_block_scale<kBits>(v[u]);
+    const float s = mx_scale(sb == 255u ? 127u : sb);
     if (at[u].row < rows) {
       const uint64_t dst = at[u].row * uint64_t(upr) * kBits + uint64_t(at[u].col) * kBits / 8u;
       if constexpr (kBits == 8) {
-        u32x2v out;
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-          v2s r = {0, 0};
-          r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, mx_bf2(v[u][2 * h]), s, false);
-          r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, mx_bf2(v[u][2 * h + 1]), s, true);
-          out[h] = __builtin_bit_cast(uint32_t, r);
-        }
-        *reinterpret_cast<u32x2v*>(q + dst) = out;
+        *reinterpret_cast<u32x2v*>(q + dst) = mx8_codes(v[u], s);
       } else {
         uint32_t r = 0u;
         r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, mx_bf2(v[u][0]), s, 0);
