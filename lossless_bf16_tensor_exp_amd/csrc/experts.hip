@@ -213,7 +213,7 @@ __global__ __launch_bounds__(256) void k_dispatch(RowArgs p) {
   const uint32_t kp = uint32_t(mx_pitch(p.cols));
   const uint32_t end = p.q ? kp : p.cols;
   for (uint32_t col = t * 8u; col < end; col += 8u << p.lt) {
-    const u32x4v v = row_load8(x, col, p.cols);
+    const u32x4v v = row_get8<!kWave>(x, col, p.cols);
     u32x2v codes = {0u, 0u};
     uint32_t sb = 0u;
     if (p.q) {
@@ -233,31 +233,52 @@ __global__ __launch_bounds__(256) void k_dispatch(RowArgs p) {
   }
 }
 
-// Eight FP32 values from column `col` of a BF16 or FP32 row, zeros behind it.
-template <bool kF32>
-__device__ __forceinline__ void row_values8(const void* rows, uint64_t at, uint32_t col, uint32_t cols, float (&v)[8]) {
-  if constexpr (kF32) {
-    const float* r = static_cast<const float*>(rows) + at;
-    if (col + 8u <= cols) {
-      const v4f a = *reinterpret_cast<const v4fa4*>(r + col), b = *reinterpret_cast<const v4fa4*>(r + col + 4u);
+// Eight values of a BF16 or FP32 row, zeros behind its end: all loads first, as
+// row_load8 and row_mend8.
+template <bool kF32, bool kTiny = true>
+struct Row8 {
+  u32x4v lo, hi;  // BF16: lo alone
+  template <bool kStream = false>
+  __device__ __forceinline__ void load(const void* rows, uint64_t at, uint32_t col, uint32_t cols) {
+    if constexpr (kF32) {
+      const float* r = static_cast<const float*>(rows) + at;
+      if (kTiny && cols < 8u) {
+        lo = hi = u32x4v{0u, 0u, 0u, 0u};
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        v[i] = a[i];
-        v[4 + i] = b[i];
+        for (uint32_t i = 0; i < 4u; i++) {
+          if (col + i < cols) lo[i] = __float_as_uint(r[col + i]);
+          if (col + 4u + i < cols) hi[i] = __float_as_uint(r[col + 4u + i]);
+        }
+      } else {
+        const float* f = r + min(col, cols - 8u);
+        const v4fa4 *a = reinterpret_cast<const v4fa4*>(f), *b = reinterpret_cast<const v4fa4*>(f + 4);
+        lo = __builtin_bit_cast(u32x4v, kStream ? v4f(__builtin_nontemporal_load(a)) : v4f(*a));
+        hi = __builtin_bit_cast(u32x4v, kStream ? v4f(__builtin_nontemporal_load(b)) : v4f(*b));
       }
     } else {
-#pragma unroll
-      for (uint32_t i = 0; i < 8u; i++) v[i] = col + i < cols ? r[col + i] : 0.0f;
-    }
-  } else {
-    const u32x4v w = row_load8(static_cast<const uint16_t*>(rows) + at, col, cols);
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      v[2 * i] = bf_lo(w[i]);
-      v[2 * i + 1] = bf_hi(w[i]);
+      lo = row_load8<kStream, kTiny>(static_cast<const uint16_t*>(rows) + at, col, cols);
     }
   }
-}
+  __device__ __forceinline__ void mend(uint32_t col, uint32_t cols) {
+    if constexpr (kF32) {
+      if (col + 8u <= cols || (kTiny && cols < 8u)) return;
+      const uint32_t by = col - (cols - 8u);
+      const u32x4v none = {0u, 0u, 0u, 0u};
+      if (by & 4u) lo = hi, hi = none;
+      if (by & 2u) lo = u32x4v{lo[2], lo[3], hi[0], hi[1]}, hi = u32x4v{hi[2], hi[3], 0u, 0u};
+      if (by & 1u) lo = u32x4v{lo[1], lo[2], lo[3], hi[0]}, hi = u32x4v{hi[1], hi[2], hi[3], 0u};
+      if (by >= 8u) lo = hi = none;
+    } else {
+      row_mend8<kTiny>(lo, col, cols);
+    }
+  }
+  __device__ __forceinline__ float value(int i) const {
+    if constexpr (kF32) return __uint_as_float(i < 4 ? lo[i] : hi[i - 4]);
+    else return i & 1 ? bf_hi(lo[i / 2]) : bf_lo(lo[i / 2]);
+  }
+};
+
+constexpr uint32_t kRowsAtOnce = 4u;  // of a token's, all their loads in flight
 
 template <bool kWave, bool kF32>
 __global__ __launch_bounds__(256) void k_combine(RowArgs p) {
@@ -267,23 +288,33 @@ __global__ __launch_bounds__(256) void k_combine(RowArgs p) {
   const int32_t* place = p.place + uint64_t(token) * p.choices;
   const float* weights = p.weights ? p.weights + uint64_t(token) * p.choices : nullptr;
   for (uint32_t col = t * 8u; col < p.cols; col += 8u << p.lt) {
-    float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    if (p.residual) row_values8<false>(p.residual, uint64_t(token) * p.ldr, col, p.cols, sum);
-    for (uint32_t j0 = 0; j0 < p.choices; j0 += 4u) {
-      float v[4][8], w[4];
-      bool has[4];
+    float sum[8];
+    Row8<false, !kWave> r;
+    if (p.residual) r.load(p.residual, uint64_t(token) * p.ldr, col, p.cols);
+    for (uint32_t j0 = 0; j0 < p.choices; j0 += kRowsAtOnce) {
+      Row8<kF32, !kWave> v[kRowsAtOnce];
+      float w[kRowsAtOnce];
+      bool has[kRowsAtOnce];
 #pragma unroll
-      for (uint32_t i = 0; i < 4u; i++) {
+      for (uint32_t i = 0; i < kRowsAtOnce; i++) {
         const uint32_t at = j0 + i < p.choices ? uint32_t(place[j0 + i]) : ~0u;
         has[i] = at < p.slots;
         w[i] = has[i] && weights ? weights[j0 + i] : 1.0f;
-        if (has[i]) row_values8<kF32>(p.rows, uint64_t(at) * p.ldrows, col, p.cols, v[i]);
+        if (has[i]) v[i].template load<kWave>(p.rows, uint64_t(at) * p.ldrows, col, p.cols);
+      }
+      loads_first();
+      if (j0 == 0u) {
+        if (p.residual) r.mend(col, p.cols);
+#pragma unroll
+        for (int c = 0; c < 8; c++) sum[c] = p.residual ? r.value(c) : 0.0f;
       }
 #pragma unroll
-      for (uint32_t i = 0; i < 4u; i++)
-        if (has[i])
+      for (uint32_t i = 0; i < kRowsAtOnce; i++)
+        if (has[i]) {
+          v[i].mend(col, p.cols);
 #pragma unroll
-          for (int c = 0; c < 8; c++) sum[c] = fmaf(w[i], v[i][c], sum[c]);
+          for (int c = 0; c < 8; c++) sum[c] = fmaf(w[i], v[i].value(c), sum[c]);
+        }
     }
     const uint64_t to = uint64_t(token) * p.ldo;
     if (p.out_f32) {
@@ -303,10 +334,10 @@ __global__ __launch_bounds__(256) void k_combine(RowArgs p) {
   }
 }
 
-// The choices go four at a time, dout read again for each four.
+// dout is read again for each kRowsAtOnce of the choices.
 template <bool kWave, bool kF32>
 __global__ __launch_bounds__(256) void k_combine_back(RowArgs p) {
-  __shared__ float part[2][4][4];
+  __shared__ float part[2][4][kRowsAtOnce];
   uint32_t t;
   const uint32_t token = row_token<kWave>(p, t);
   const bool live = token < p.tokens;
@@ -314,57 +345,65 @@ __global__ __launch_bounds__(256) void k_combine_back(RowArgs p) {
   const float* weights = p.weights ? p.weights + uint64_t(live ? token : 0u) * p.choices : nullptr;
   const uint16_t* x = p.x + uint64_t(live ? token : 0u) * p.ldx;
   const uint32_t span = min(1u << p.lt, 64u);
-  for (uint32_t j0 = 0, turn = 0; j0 < p.choices; j0 += 4u, turn ^= 1u) {
-    uint32_t at[4];
-    float w[4], dot[4];
+  for (uint32_t j0 = 0, turn = 0; j0 < p.choices; j0 += kRowsAtOnce, turn ^= 1u) {
+    uint32_t at[kRowsAtOnce];
+    float w[kRowsAtOnce], dot[kRowsAtOnce];
 #pragma unroll
-    for (uint32_t i = 0; i < 4u; i++) {
+    for (uint32_t i = 0; i < kRowsAtOnce; i++) {
       at[i] = live && j0 + i < p.choices ? uint32_t(place[j0 + i]) : ~0u;
       w[i] = at[i] < p.slots && weights ? weights[j0 + i] : 1.0f;
       dot[i] = 0.0f;
     }
     for (uint32_t col = t * 8u; live && col < p.cols; col += 8u << p.lt) {
-      float d[8];
-      row_values8<false>(x, 0u, col, p.cols, d);
+      Row8<false, !kWave> d;
+      Row8<kF32, !kWave> v[kRowsAtOnce];
+      d.load(x, 0u, col, p.cols);
       if (p.dweights) {
-        float v[4][8];
 #pragma unroll
-        for (uint32_t i = 0; i < 4u; i++)
-          if (at[i] < p.slots) row_values8<kF32>(p.rows, uint64_t(at[i]) * p.ldrows, col, p.cols, v[i]);
-#pragma unroll
-        for (uint32_t i = 0; i < 4u; i++)
-          if (at[i] < p.slots)
-#pragma unroll
-            for (int c = 0; c < 8; c++) dot[i] = fmaf(d[c], v[i][c], dot[i]);
+        for (uint32_t i = 0; i < kRowsAtOnce; i++)
+          if (at[i] < p.slots) v[i].template load<kWave>(p.rows, uint64_t(at[i]) * p.ldrows, col, p.cols);
       }
+      loads_first();
+      d.mend(col, p.cols);
       if (p.out) {
 #pragma unroll
-        for (uint32_t i = 0; i < 4u; i++)
-          if (at[i] < p.slots)
-            row_store8(static_cast<uint16_t*>(p.out) + uint64_t(at[i]) * p.ldo, col, p.cols,
-                       u32x4v{mx_bf16x2(w[i] * d[0], w[i] * d[1]), mx_bf16x2(w[i] * d[2], w[i] * d[3]),
-                              mx_bf16x2(w[i] * d[4], w[i] * d[5]), mx_bf16x2(w[i] * d[6], w[i] * d[7])});
+        for (uint32_t i = 0; i < kRowsAtOnce; i++)
+          if (at[i] < p.slots) {
+            u32x4v o;
+#pragma unroll
+            for (int c = 0; c < 4; c++) o[c] = mx_bf16x2(w[i] * d.value(2 * c), w[i] * d.value(2 * c + 1));
+            row_store8<kWave>(static_cast<uint16_t*>(p.out) + uint64_t(at[i]) * p.ldo, col, p.cols, o);
+          }
+      }
+      if (p.dweights) {
+#pragma unroll
+        for (uint32_t i = 0; i < kRowsAtOnce; i++)
+          if (at[i] < p.slots) {
+            v[i].mend(col, p.cols);
+#pragma unroll
+            for (int c = 0; c < 8; c++) dot[i] = fmaf(d.value(c), v[i].value(c), dot[i]);
+          }
       }
     }
     if (!p.dweights) continue;
+    for (uint32_t s = span >> 1; s > 0u; s >>= 1)
 #pragma unroll
-    for (uint32_t i = 0; i < 4u; i++)
-      for (uint32_t s = span >> 1; s > 0u; s >>= 1) dot[i] += __shfl_xor(dot[i], int(s));
+      for (uint32_t i = 0; i < kRowsAtOnce; i++) dot[i] += __shfl_xor(dot[i], int(s));
     if (p.lt > 6u) {
       if ((threadIdx.x & 63u) == 0u)
 #pragma unroll
-        for (uint32_t i = 0; i < 4u; i++) part[turn][threadIdx.x >> 6][i] = dot[i];
+        for (uint32_t i = 0; i < kRowsAtOnce; i++) part[turn][threadIdx.x >> 6][i] = dot[i];
       __syncthreads();
       const uint32_t waves = 1u << (p.lt - 6u), w0 = threadIdx.x >> 6 & ~(waves - 1u);
 #pragma unroll
-      for (uint32_t i = 0; i < 4u; i++) {
+      for (uint32_t i = 0; i < kRowsAtOnce; i++) {
         dot[i] = 0.0f;
         for (uint32_t k = 0; k < waves; k++) dot[i] += part[turn][w0 + k][i];
       }
     }
     if (live && t == 0u)
 #pragma unroll
-      for (uint32_t i = 0; i < 4u; i++)
+      for (uint32_t i = 0; i < kRowsAtOnce; i++)
         if (j0 + i < p.choices) p.dweights[uint64_t(token) * p.choices + j0 + i] = at[i] < p.slots ? dot[i] : 0.0f;
   }
 }

@@ -19,6 +19,8 @@ namespace {
 
 constexpr uint32_t kLowRankMax = 128u;
 constexpr uint32_t kLowRankRows = 16u;
+constexpr uint32_t kLowRankThreads = 512u;
+constexpr uint32_t kLowRankSlab = kLowRankThreads;  // columns that the waves take at once
 
 struct LowRankArgs {
   const uint16_t* x;
@@ -67,19 +69,22 @@ __device__ __forceinline__ bool low_rank_rows(const LowRankArgs& p, uint32_t g, 
 // tiles, 64 lists a step.
 __device__ __forceinline__ bool low_rank_tile(const LowRankArgs& p, uint32_t& g, uint32_t& row0, uint32_t& row1, uint32_t& slab) {
   const uint32_t lane = threadIdx.x & 63u, lists = p.adapters + 2u;
-  uint32_t r0 = 0u, r1 = 0u, sum = 0u, total = 0u;
-  for (uint32_t c = 0; c < lists; c += 64u) {
+  uint32_t r0 = 0u, r1 = 0u, own = 0u, sum = 0u, total = 0u;
+  const auto count = [&](uint32_t c) {
     low_rank_rows(p, c + lane, r0, r1);
-    total += uint32_t(__builtin_amdgcn_readlane(int(mx_scan((r1 - r0 + kLowRankRows - 1u) / kLowRankRows)), 63));
+    own = (r1 - r0 + kLowRankRows - 1u) / kLowRankRows;
+    sum = wave_incl_scan(own);
+  };
+  for (uint32_t c = 0; c < lists; c += 64u) {
+    count(c);
+    total += uint32_t(__builtin_amdgcn_readlane(int(sum), 63));
   }
   if (blockIdx.x >= total * p.slabs) return false;
   const uint32_t at = mx_xcd_run(blockIdx.x, total * p.slabs), tile = at / p.slabs;
   slab = at - tile * p.slabs;
   uint32_t before = 0u;
   for (uint32_t c = 0; c < lists; c += 64u) {
-    low_rank_rows(p, c + lane, r0, r1);
-    const uint32_t own = (r1 - r0 + kLowRankRows - 1u) / kLowRankRows;
-    sum = mx_scan(own);
+    if (lists > 64u) count(c);
     const uint64_t past = __ballot(before + sum > tile);
     if (past) {
       const int l = __ffsll((unsigned long long)past) - 1;
@@ -109,44 +114,6 @@ __device__ __forceinline__ void low_rank_report(const LowRankArgs& p) {
   }
 }
 
-// Sixteen neighbouring columns of a row: base, or zeros without one.
-__device__ __forceinline__ void low_rank_base(const LowRankArgs& p, uint64_t row, uint32_t col, float (&v)[16]) {
-  if (!p.base || col >= p.n) {
-#pragma unroll
-    for (int i = 0; i < 16; i++) v[i] = 0.0f;
-    return;
-  }
-#pragma unroll
-  for (uint32_t h = 0; h < 2u; h++) {
-    float e[8];
-    if (p.base_f32) row_values8<true>(p.base, row * p.ldb, col + 8u * h, p.n, e);
-    else row_values8<false>(p.base, row * p.ldb, col + 8u * h, p.n, e);
-#pragma unroll
-    for (uint32_t i = 0; i < 8u; i++) v[8u * h + i] = e[i];
-  }
-}
-__device__ __forceinline__ void low_rank_store(const LowRankArgs& p, uint64_t row, uint32_t col, const float (&v)[16]) {
-#pragma unroll
-  for (uint32_t h = 0; h < 2u; h++) {
-    const uint32_t c = col + 8u * h;
-    const float* e = v + 8u * h;
-    if (p.y_f32) {
-      float* o = static_cast<float*>(p.y) + row * p.ldy + c;
-      if (c + 8u <= p.n) {
-        *reinterpret_cast<v4fa4*>(o) = v4f{e[0], e[1], e[2], e[3]};
-        *reinterpret_cast<v4fa4*>(o + 4) = v4f{e[4], e[5], e[6], e[7]};
-      } else {
-#pragma unroll
-        for (uint32_t i = 0; i < 7u; i++)
-          if (c + i < p.n) o[i] = e[i];
-      }
-    } else {
-      row_store8(static_cast<uint16_t*>(p.y) + row * p.ldy, c, p.n,
-                 u32x4v{mx_bf16x2(e[0], e[1]), mx_bf16x2(e[2], e[3]), mx_bf16x2(e[4], e[5]), mx_bf16x2(e[6], e[7])});
-    }
-  }
-}
-
 // v as three BF16 numbers whose sum it is: its leading 8 significant bits, the
 // next 8 and the last.  Cut, not rounded, so that none passes BF16's range;
 // an infinity or a NaN is the first alone.
@@ -163,109 +130,333 @@ __device__ __forceinline__ void low_rank_split(float v, uint16_t (&part)[3]) {
   part[2] = mx_bf16(r - __uint_as_float(__float_as_uint(r) & 0xFFFF0000u));
 }
 
-// kF: fragments of 16 ranks (1, 2, 4 or 8).
+// LDS of a wave alone: what its lanes wrote before is what they read after.
+__device__ __forceinline__ void wave_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// Where wave `wave` of kW begins in from .. to - 1, each with a stretch of whole
+// 64s of its own, and where it ends.
+template <uint32_t kW>
+__device__ __forceinline__ void low_rank_share(uint32_t wave, uint32_t from, uint32_t to, uint32_t& c, uint32_t& end) {
+  const uint32_t each = ((to - from + kW * 64u - 1u) / (kW * 64u)) * 64u;
+  c = min(from + wave * each, to);
+  end = min(c + each, to);
+}
+
+// The row of x or y of the tile's row `at`; false where it has none.
+__device__ __forceinline__ bool low_rank_row(const LowRankArgs& p, uint32_t row0, uint32_t row1, uint32_t at, uint32_t& row) {
+  const uint32_t slot = min(row0 + at, row1 - 1u);
+  row = p.order ? uint32_t(p.order[slot]) : slot;
+  const bool live = row0 + at < row1 && row < p.tokens;
+  if (row >= p.tokens) row = 0u;
+  return live;
+}
+
+// v = A x: a wave's part of the contraction, for 16 rows.  The rows come from
+// memory as they lie, neighbouring lanes on neighbouring bytes, and go through
+// LDS into the order of the matrix instructions, whose neighbouring lanes hold
+// neighbouring rows (loaded in that order each lane's 16 bytes are a request of
+// their own: 16,384 rows, k = n = 2,048, rank 16: 60 us instead of 48; 4,001 rows at rank
+// 64: 24 instead of 18).
 template <uint32_t kF>
-__global__ __launch_bounds__(256) void k_low_rank(LowRankArgs p) {
-  constexpr uint32_t kR = kF * 16u;              // ranks, zeros behind the real ones
-  constexpr uint32_t kLine = (kF == 1u ? 16u : kR) + 8u;  // of a row's parts in LDS, 16 bytes more for the banks
-  __shared__ float sums[4][kR][kLowRankRows];
+struct LowRankInner {
+  static constexpr uint32_t kR = kF * 16u;
+  static constexpr uint32_t kStep = kF <= 2u ? 64u : 32u;  // values of k at a time
+  static constexpr uint32_t kRow = kStep * 2u;             // bytes of a row of them
+  static constexpr uint32_t kChunks = kRow / 16u, kPer = 64u / kChunks;  // lanes on a row, rows a load
+  static constexpr uint32_t kX = kLowRankRows / kPer, kA = kR / kPer;    // loads
+  static constexpr uint32_t kLds = (kLowRankRows + kR) * kRow;
+  const uint16_t* x[kX];
+  const uint16_t* a[kA];
+  u32x4v wx[kX], wa[kA];
+  __device__ __forceinline__ void rows(const LowRankArgs& p, uint32_t g, uint32_t row0, uint32_t row1) {
+    const uint32_t r = (threadIdx.x & 63u) / kChunks;
+#pragma unroll
+    for (uint32_t i = 0; i < kA; i++) a[i] = p.a + (uint64_t(g) * p.rank + min(i * kPer + r, p.rank - 1u)) * p.k;
+#pragma unroll
+    for (uint32_t i = 0; i < kX; i++) {
+      uint32_t row;
+      low_rank_row(p, row0, row1, i * kPer + r, row);
+      x[i] = p.x + uint64_t(row) * p.ldx;
+    }
+  }
+  __device__ __forceinline__ void load(uint32_t c, uint32_t k) {
+    const uint32_t at = c + (threadIdx.x % kChunks) * 8u;
+#pragma unroll
+    for (uint32_t i = 0; i < kX; i++) wx[i] = row_load8(x[i], at, k);
+#pragma unroll
+    for (uint32_t i = 0; i < kA; i++) wa[i] = row_load8(a[i], at, k);
+    loads_first();
+  }
+  __device__ __forceinline__ void run(uint8_t* lds, uint32_t c, uint32_t end, uint32_t k, v4f (&acc)[kF]) {
+    const uint32_t lane = threadIdx.x & 63u, i16 = lane & 15u, quarter = lane >> 4;
+    const uint32_t r = lane / kChunks, chunk = lane % kChunks;
+#pragma unroll
+    for (uint32_t f = 0; f < kF; f++) acc[f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    if (c < end) load(c, k);
+    for (; c < end; c += kStep) {
+      if (c + kStep > k) {
+#pragma unroll
+        for (uint32_t i = 0; i < kX; i++) row_mend8(wx[i], c + chunk * 8u, k);
+#pragma unroll
+        for (uint32_t i = 0; i < kA; i++) row_mend8(wa[i], c + chunk * 8u, k);
+      }
+#pragma unroll
+      for (uint32_t i = 0; i < kX; i++) *reinterpret_cast<u32x4v*>(lds + mx_at<kRow>(i * kPer + r, chunk)) = wx[i];
+#pragma unroll
+      for (uint32_t i = 0; i < kA; i++)
+        *reinterpret_cast<u32x4v*>(lds + mx_at<kRow>(kLowRankRows + i * kPer + r, chunk)) = wa[i];
+      if (c + kStep < end) load(c + kStep, k);
+      wave_lds();
+#pragma unroll
+      for (uint32_t h = 0; h < kStep / 32u; h++) {
+        const v8bf bx = *reinterpret_cast<const v8bf*>(lds + mx_at<kRow>(i16, h * 4u + quarter));
+#pragma unroll
+        for (uint32_t f = 0; f < kF; f++)
+          acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              *reinterpret_cast<const v8bf*>(lds + mx_at<kRow>((f + 1u) * 16u + i16, h * 4u + quarter)), bx, acc[f], 0, 0, 0);
+      }
+      wave_lds();
+    }
+  }
+};
+
+// y = base + B v, 64 columns a step: B's rows through LDS likewise, 32 ranks at a
+// time.  Row 4 j + f of the 64 is column j of matrix fragment f, so that a lane
+// ends with four neighbouring columns of four rows, and 16 lanes with 64.  16
+// ranks fill half a matrix instruction: the other half takes v's next part.
+template <uint32_t kF, bool kF32>
+struct LowRankOuter {
+  static constexpr uint32_t kR = kF * 16u;
+  static constexpr uint32_t kP = kF == 1u ? 1u : kF / 2u;  // pieces of ranks
+  static constexpr uint32_t kSteps = kF == 1u ? 2u : kP * 3u;
+  static constexpr uint32_t kRow = kF == 1u ? 32u : 64u;   // bytes of a row's piece
+  static constexpr uint32_t kChunks = kRow / 16u, kPer = 64u / kChunks, kLoads = 64u / kPer;
+  static constexpr uint32_t kFrag = 17u * kRow;            // bytes from one fragment to the next
+  static constexpr uint32_t kLds = 4u * kFrag;
+  const uint16_t* b;
+  uint64_t row[4];
+  bool live[4];
+  u32x4v w[kLoads];
+  u32x4v base[4];  // BF16: the first half
+  static __device__ __forceinline__ uint32_t at(uint32_t f, uint32_t j, uint32_t chunk) {
+    const uint32_t turn = kF == 1u ? j >> 3 : j >> 2;
+    return f * kFrag + j * kRow + ((chunk ^ turn) * 16u);
+  }
+  __device__ __forceinline__ void rows(const LowRankArgs& p, uint32_t g, uint32_t row0, uint32_t row1) {
+    b = p.b + uint64_t(g) * p.n * p.rank;
+#pragma unroll
+    for (uint32_t r = 0; r < 4u; r++) {
+      uint32_t of;
+      live[r] = low_rank_row(p, row0, row1, ((threadIdx.x >> 4) & 3u) * 4u + r, of);
+      row[r] = of;
+    }
+  }
+  __device__ __forceinline__ void load_b(const LowRankArgs& p, uint32_t c, uint32_t piece) {
+    const uint32_t lane = threadIdx.x & 63u;
+#pragma unroll
+    for (uint32_t i = 0; i < kLoads; i++)
+      w[i] = row_load8(b + uint64_t(min(c + i * kPer + lane / kChunks, p.n - 1u)) * p.rank, piece * 32u + lane % kChunks * 8u, p.rank);
+  }
+  // this lane's four columns of its four rows: whole where none passes the end
+  __device__ __forceinline__ void load_base(const LowRankArgs& p, uint32_t c) {
+    const uint32_t col = c + (threadIdx.x & 15u) * 4u;
+    if (!p.base) return;
+#pragma unroll
+    for (uint32_t r = 0; r < 4u; r++) {
+      const uint64_t from = row[r] * p.ldb + col;
+      if constexpr (kF32) {
+        const float* f = static_cast<const float*>(p.base) + from;
+        if (col + 4u <= p.n) {
+          base[r] = __builtin_bit_cast(u32x4v, v4f(*reinterpret_cast<const v4fa4*>(f)));
+        } else {
+#pragma unroll
+          for (uint32_t i = 0; i < 4u; i++) base[r][i] = col + i < p.n ? __float_as_uint(f[i]) : 0u;
+        }
+      } else {
+        const uint16_t* f = static_cast<const uint16_t*>(p.base) + from;
+        if (col + 4u <= p.n) {
+          const u32x2v v = *reinterpret_cast<const u32x2a2*>(f);
+          base[r][0] = v[0];
+          base[r][1] = v[1];
+        } else {
+          base[r][0] = (col < p.n ? uint32_t(f[0]) : 0u) | (col + 1u < p.n ? uint32_t(f[1]) << 16 : 0u);
+          base[r][1] = col + 2u < p.n ? uint32_t(f[2]) : 0u;
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ float value(const LowRankArgs& p, uint32_t r, uint32_t i) const {
+    if (!p.base) return 0.0f;
+    if constexpr (kF32) return __uint_as_float(base[r][i]);
+    else return i & 1u ? bf_hi(base[r][i >> 1]) : bf_lo(base[r][i >> 1]);
+  }
+  __device__ __forceinline__ void store(const LowRankArgs& p, uint32_t c, const v4f (&sum)[4], bool add) {
+    const uint32_t col = c + (threadIdx.x & 15u) * 4u;
+#pragma unroll
+    for (uint32_t r = 0; r < 4u; r++) {
+      float v[4];
+#pragma unroll
+      for (uint32_t f = 0; f < 4u; f++) v[f] = add ? value(p, r, f) + sum[f][r] : value(p, r, f);
+      if (!live[r]) continue;
+      const uint64_t to = row[r] * p.ldy + col;
+      if (p.y_f32) {
+        float* o = static_cast<float*>(p.y) + to;
+        if (col + 4u <= p.n) {
+          *reinterpret_cast<v4fa4*>(o) = v4f{v[0], v[1], v[2], v[3]};
+        } else {
+#pragma unroll
+          for (uint32_t i = 0; i < 3u; i++)
+            if (col + i < p.n) o[i] = v[i];
+        }
+      } else {
+        uint16_t* o = static_cast<uint16_t*>(p.y) + to;
+        if (col + 4u <= p.n) {
+          *reinterpret_cast<u32x2a2*>(o) = u32x2v{mx_bf16x2(v[0], v[1]), mx_bf16x2(v[2], v[3])};
+        } else {
+#pragma unroll
+          for (uint32_t i = 0; i < 3u; i++)
+            if (col + i < p.n) o[i] = mx_bf16(v[i]);
+        }
+      }
+    }
+  }
+  // rows of no adapter: base alone
+  __device__ __forceinline__ void bare(const LowRankArgs& p, uint32_t c, uint32_t n1) {
+    const v4f none[4] = {};
+    for (; c < n1; c += 64u) {
+      load_base(p, c);
+      store(p, c, none, false);
+    }
+  }
+  // columns c .. n1 - 1, B and base of the first 64 being loaded
+  __device__ __forceinline__ void columns(const LowRankArgs& p, uint8_t* lds, const v8bf (&v)[kSteps], uint32_t c, uint32_t n1) {
+    const uint32_t lane = threadIdx.x & 63u, i16 = lane & 15u, quarter = lane >> 4;
+    for (; c < n1; c += 64u) {
+      v4f sum[4];
+#pragma unroll
+      for (uint32_t f = 0; f < 4u; f++) sum[f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (uint32_t piece = 0; piece < kP; piece++) {
+        if (p.rank != kR) {
+#pragma unroll
+          for (uint32_t i = 0; i < kLoads; i++) row_mend8(w[i], piece * 32u + lane % kChunks * 8u, p.rank);
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < kLoads; i++) {
+          const uint32_t n = i * kPer + lane / kChunks;
+          *reinterpret_cast<u32x4v*>(lds + at(n & 3u, n >> 2, lane % kChunks)) = w[i];
+        }
+        if (piece + 1u < kP) load_b(p, c, piece + 1u);
+        else if (c + 64u < n1) load_b(p, c + 64u, 0u);
+        loads_first();
+        wave_lds();
+#pragma unroll
+        for (uint32_t f = 0; f < 4u; f++) {
+          const v8bf fb = *reinterpret_cast<const v8bf*>(lds + at(f, i16, kF == 1u ? quarter & 1u : quarter));
+          if constexpr (kF == 1u) {
+            sum[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[1], fb, sum[f], 0, 0, 0);
+            sum[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[0], fb, sum[f], 0, 0, 0);
+          } else {
+#pragma unroll
+            for (uint32_t part = 3u; part > 0u; part--)  // the smallest part first
+              sum[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[(part - 1u) * kP + piece], fb, sum[f], 0, 0, 0);
+          }
+        }
+        wave_lds();
+      }
+      store(p, c, sum, true);
+      if (c + 64u < n1) load_base(p, c + 64u);
+    }
+  }
+};
+
+// kF: fragments of 16 ranks (1, 2, 4 or 8).
+template <uint32_t kF, bool kF32>
+__global__ __launch_bounds__(kLowRankThreads) void k_low_rank(LowRankArgs p) {
+  typedef LowRankInner<kF> Inner;
+  typedef LowRankOuter<kF, kF32> Outer;
+  constexpr uint32_t kW = kLowRankThreads / 64u;
+  constexpr uint32_t kR = kF * 16u;    // ranks, zeros behind the real ones
+  constexpr uint32_t kLine = kR + 8u;  // of a row's parts in LDS, 16 bytes more for the banks
+  constexpr uint32_t kSum = kR + 4u;   // of a row's sums, likewise
+  constexpr uint32_t kMine = Inner::kLds > Outer::kLds ? Inner::kLds : Outer::kLds;
+  constexpr uint32_t kSums = kW * kLowRankRows * kSum * 4u;
+  __shared__ __attribute__((aligned(256))) uint8_t lds[kW * kMine > kSums ? kW * kMine : kSums];
   __shared__ __attribute__((aligned(16))) uint16_t parts[3][kLowRankRows][kLine];
   const uint32_t tid = threadIdx.x, lane = tid & 63u, i16 = lane & 15u, quarter = lane >> 4;
   const uint32_t wave = mx_first(tid >> 6);
   if (blockIdx.x == 0u) low_rank_report(p);
   uint32_t g, row0, row1, slab;
   if (!low_rank_tile(p, g, row0, row1, slab)) return;
-  const uint32_t n0 = slab * p.slab, n1 = min(p.n, n0 + p.slab);
-  const uint32_t slot = min(row0 + i16, row1 - 1u);
-  const uint32_t named = p.order ? uint32_t(p.order[slot]) : slot;
-  const bool live = row0 + i16 < row1 && named < p.tokens;
-  const uint64_t row = named < p.tokens ? named : 0u;
-  float v[16];
+  uint32_t c, n1;
+  low_rank_share<kW>(wave, slab * p.slab, min(p.n, (slab + 1u) * p.slab), c, n1);
+  Outer o;
   if (g >= p.adapters) {  // no adapter
     if (p.base == p.y) return;
-    for (uint32_t c = n0 + wave * 64u; c < n1; c += 256u) {
-      low_rank_base(p, row, c + quarter * 16u, v);
-      if (live) low_rank_store(p, row, c + quarter * 16u, v);
-    }
+    o.rows(p, 0u, row0, row1);
+    o.bare(p, c, n1);
     return;
   }
-
-  // v = A x: lanes hold 16 neighbouring values of k, of a rank and of a row,
-  // for two matrix instructions (the contraction's order is the same for both
-  // operands); the waves take turns of 64
-  const uint16_t* a = p.a + uint64_t(g) * p.rank * p.k;
-  const uint16_t* x = p.x + row * p.ldx;
+  Inner in;
+  in.rows(p, g, row0, row1);
   v4f acc[kF];
-#pragma unroll
-  for (uint32_t f = 0; f < kF; f++) acc[f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 2
-  for (uint32_t c = wave * 64u; c < p.k; c += 256u) {
-    const uint32_t at = c + quarter * 16u;
-    const v8bf x0 = __builtin_bit_cast(v8bf, row_load8(x, at, p.k)), x1 = __builtin_bit_cast(v8bf, row_load8(x, at + 8u, p.k));
-#pragma unroll
-    for (uint32_t f = 0; f < kF; f++) {
-      const uint16_t* ar = a + uint64_t(min(f * 16u + i16, p.rank - 1u)) * p.k;
-      acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, row_load8(ar, at, p.k)), x0, acc[f], 0, 0, 0);
-      acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, row_load8(ar, at + 8u, p.k)), x1, acc[f], 0, 0, 0);
-    }
+  uint32_t k0, k1;
+  low_rank_share<kW>(wave, 0u, p.k, k0, k1);
+  in.run(lds + wave * kMine, k0, k1, p.k, acc);
+  o.rows(p, g, row0, row1);
+  if (c < n1) {  // meanwhile
+    o.load_b(p, c, 0u);
+    o.load_base(p, c);
+    loads_first();
   }
+  __syncthreads();
+  float* sums = reinterpret_cast<float*>(lds);
 #pragma unroll
   for (uint32_t f = 0; f < kF; f++)
-#pragma unroll
-    for (uint32_t r = 0; r < 4u; r++) sums[wave][f * 16u + quarter * 4u + r][i16] = acc[f][r];
+    *reinterpret_cast<v4f*>(sums + (wave * kLowRankRows + i16) * kSum + f * 16u + quarter * 4u) = acc[f];
   __syncthreads();
   const float s = p.scales ? p.scales[g] : 1.0f;
+  for (uint32_t i = tid; i < kR * kLowRankRows; i += kLowRankThreads) {
+    const uint32_t t = i / kR, r = i % kR;
+    float sum = sums[t * kSum + r];
 #pragma unroll
-  for (uint32_t i = 0; i < kF; i++) {
-    const uint32_t r = i * 16u + (tid >> 4);
-    const float sum = s * (sums[0][r][i16] + sums[1][r][i16] + sums[2][r][i16] + sums[3][r][i16]);
+    for (uint32_t w = 1; w < kW; w++) sum += sums[(w * kLowRankRows + t) * kSum + r];
     uint16_t part[3];
-    low_rank_split(r < p.rank ? sum : 0.0f, part);
+    low_rank_split(r < p.rank ? s * sum : 0.0f, part);
 #pragma unroll
-    for (int j = 0; j < 3; j++) parts[j][i16][r] = part[j];
+    for (int j = 0; j < 3; j++) parts[j][t][r] = part[j];
   }
   __syncthreads();
-
-  // y = base + B v.  Row i of fragment f is column 16 (i / 4) + 4 f + i % 4 of
-  // the wave's 64, so that a lane's sums of four fragments are 16 neighbours.
-  // 16 ranks fill half an instruction: the other half takes the next part.
-  constexpr uint32_t kSteps = kF == 1u ? 2u : kF / 2u * 3u;
-  v8bf bv[kSteps];
+  v8bf v[Outer::kSteps];
 #pragma unroll
-  for (uint32_t i = 0; i < kSteps; i++) {
+  for (uint32_t i = 0; i < Outer::kSteps; i++) {
     if constexpr (kF == 1u) {
       const uint32_t part = i * 2u + (quarter >> 1);
-      bv[i] = part < 3u ? *reinterpret_cast<const v8bf*>(&parts[part][i16][(quarter & 1u) * 8u])
-                        : __builtin_bit_cast(v8bf, u32x4v{0u, 0u, 0u, 0u});
+      v[i] = part < 3u ? *reinterpret_cast<const v8bf*>(&parts[part][i16][(quarter & 1u) * 8u])
+                       : __builtin_bit_cast(v8bf, u32x4v{0u, 0u, 0u, 0u});
     } else {
-      bv[i] = *reinterpret_cast<const v8bf*>(&parts[i / (kF / 2u)][i16][i % (kF / 2u) * 32u + quarter * 8u]);
+      v[i] = *reinterpret_cast<const v8bf*>(&parts[i / Outer::kP][i16][i % Outer::kP * 32u + quarter * 8u]);
     }
   }
-  const uint16_t* b = p.b + uint64_t(g) * p.n * p.rank;
-  for (uint32_t c = n0 + wave * 64u; c < n1; c += 256u) {
-    const uint32_t col = c + quarter * 16u;
-    low_rank_base(p, row, col, v);
-#pragma unroll
-    for (uint32_t f = 0; f < 4u; f++) {
-      const uint16_t* br = b + uint64_t(min(c + (i16 >> 2) * 16u + f * 4u + (i16 & 3u), p.n - 1u)) * p.rank;
-      v4f sum = {0.0f, 0.0f, 0.0f, 0.0f};
-      if constexpr (kF == 1u) {
-        const v8bf w = __builtin_bit_cast(v8bf, row_load8(br, (quarter & 1u) * 8u, p.rank));
-        sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, bv[1], sum, 0, 0, 0);
-        sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, bv[0], sum, 0, 0, 0);
-      } else {
-        v8bf w[kF / 2u];
-#pragma unroll
-        for (uint32_t i = 0; i < kF / 2u; i++) w[i] = __builtin_bit_cast(v8bf, row_load8(br, i * 32u + quarter * 8u, p.rank));
-#pragma unroll
-        for (uint32_t i = kSteps; i > 0u; i--)
-          sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[(i - 1u) % (kF / 2u)], bv[i - 1u], sum, 0, 0, 0);
-      }
-#pragma unroll
-      for (uint32_t r = 0; r < 4u; r++) v[f * 4u + r] += sum[r];
-    }
-    if (live) low_rank_store(p, row, col, v);
-  }
+  o.columns(p, lds + wave * kMine, v, c, n1);
+}
+
+// Column slabs of a row tile.  Every slab makes the tile's inner values again,
+// so there are only as many as it takes to give the 256 CUs a workgroup each, and
+// half as many where the ranks make that work large.  us with 1 slab, with as
+// many as make 128, 256 and 512 workgroups (n, k, rank, tokens in adapters):
+//   2,048 x 2,048, 16, 64 in 24     8.4   6.9   6.2   6.2
+//   1,999 x 2,051, 24, 777 in 9    15.5  12.6  10.4  10.3
+//   2,048 x 2,048, 64, 4,001 in 9  18.6  18.1  18.0  23.3
+//   8,192 x 2,048, 64, 500 in 8    36.4  16.8  15.2  21.0
+//   4,096 x 4,096, 128, 1,000 in 8 48.4  38.1  57.5  75.7
+// (Inner and outer product in launches of their own, the inner values in memory
+// between them, took 4 to 10 us more than the best of these, except for 300 rows
+// of 8,192 at rank 128: 29 instead of 39.)
+uint32_t low_rank_slabs(uint64_t tiles, uint64_t n, uint64_t rank) {
+  const uint64_t most = cdiv(n, kLowRankSlab), want = tiles ? cdiv(rank > 64u ? 128u : 256u, tiles) : 1u;
+  const uint64_t slab = cdiv(cdiv(n, want < most ? want : most), kLowRankSlab) * kLowRankSlab;
+  return uint32_t(cdiv(n, slab));
 }
 
 }  // namespace
@@ -321,17 +512,22 @@ ciera_status low_rank_add(const void* d_x, uint64_t ldx, const void* d_a, const 
   // every list of rows may end in a part of a tile
   const uint64_t lists = adapters + 2ull;
   const uint64_t tiles = tokens / kLowRankRows + (lists < tokens ? lists : tokens);
-  p.slab = 512u;
-  p.slabs = uint32_t(cdiv(n, p.slab));
+  p.slabs = low_rank_slabs(tiles, n, rank);
+  p.slab = uint32_t(cdiv(cdiv(n, p.slabs), kLowRankSlab) * kLowRankSlab);
   const uint64_t grid = tiles ? tiles * p.slabs : 1u;
-  if (grid > kMxMostGroups) return CIERA_ERR_ARG;
-  (void)hipGetLastError();
-  const dim3 g(static_cast<uint32_t>(grid)), block(256);
-  if (rank <= 16u) launch(k_low_rank<1u>, g, block, stream, p);
-  else if (rank <= 32u) launch(k_low_rank<2u>, g, block, stream, p);
-  else if (rank <= 64u) launch(k_low_rank<4u>, g, block, stream, p);
-  else launch(k_low_rank<8u>, g, block, stream, p);
-  return launch_status();
+  if (grid > 0xFFFFFFFFull / kLowRankThreads) return CIERA_ERR_ARG;
+  const auto go = [&](auto frags) {
+    constexpr uint32_t kF = decltype(frags)::value;
+    const dim3 g(static_cast<uint32_t>(grid)), block(kLowRankThreads);
+    (void)hipGetLastError();
+    if (base_f32) launch(k_low_rank<kF, true>, g, block, stream, p);
+    else launch(k_low_rank<kF, false>, g, block, stream, p);
+    return launch_status();
+  };
+  if (rank <= 16u) return go(std::integral_constant<uint32_t, 1u>());
+  if (rank <= 32u) return go(std::integral_constant<uint32_t, 2u>());
+  if (rank <= 64u) return go(std::integral_constant<uint32_t, 4u>());
+  return go(std::integral_constant<uint32_t, 8u>());
 }
 
 }  // extern "C"

@@ -19,6 +19,9 @@ namespace {
 constexpr uint32_t kNormMaxCols = 32768u;  // 1,024 threads of four units of 8 values
 constexpr uint32_t kNormParts = 512u;      // workgroups of the backward pass, each with a sum of dw of its own
 
+template <uint32_t k>
+using Num = std::integral_constant<uint32_t, k>;
+
 struct NormArgs {
   const uint16_t* x;
   uint64_t ldx;
@@ -39,91 +42,150 @@ struct NormArgs {
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// Eight values of a row from column `col`, zeros behind its end.
+// Eight values of a row from column `col`, zeros behind its end, in two steps,
+// so that a thread's loads all go out before it waits for one: row_load8 reads
+// the unit, or for a unit that passes the end the row's last eight values, and
+// row_mend8 moves those to where they belong.
+// kStream: past the last-level cache.  kTiny: rows of less than 8 are possible.
+template <bool kStream = false, bool kTiny = true>
 __device__ __forceinline__ u32x4v row_load8(const uint16_t* row, uint32_t col, uint32_t cols) {
-  if (col + 8u <= cols) return u32x4v(*reinterpret_cast<const u32x4a2*>(row + col));
-  return mx_part8(row + (col < cols ? col : 0u), col < cols ? cols - col : 0u);
+  if (kTiny && cols < 8u) return mx_part8(row, col == 0u ? cols : 0u);
+  const u32x4a2* at = reinterpret_cast<const u32x4a2*>(row + min(col, cols - 8u));
+  if constexpr (kStream) return u32x4v(__builtin_nontemporal_load(at));
+  else return u32x4v(*at);
 }
-__device__ __forceinline__ void row_store8(uint16_t* row, uint32_t col, uint32_t cols, u32x4v v) {
-  if (col + 8u <= cols) {
-    *reinterpret_cast<u32x4a2*>(row + col) = v;
+// kWhole: the rows are multiples of 8 long, and a unit is theirs or is not.  No
+// branches: threads with and without a unit to mend share waves.
+template <bool kTiny = true, bool kWhole = false>
+__device__ __forceinline__ void row_mend8(u32x4v& v, uint32_t col, uint32_t cols) {
+  const u32x4v none = {0u, 0u, 0u, 0u};
+  if constexpr (kWhole) {
+    v = col < cols ? v : none;
   } else {
+    if (kTiny && cols < 8u) return;
+    const uint32_t by = col + 8u > cols ? col + 8u - cols : 0u;  // values to move down
+    v = by & 4u ? u32x4v{v[2], v[3], 0u, 0u} : v;
+    v = by & 2u ? u32x4v{v[1], v[2], v[3], 0u} : v;
+    v = by & 1u ? u32x4v{__builtin_amdgcn_alignbit(v[1], v[0], 16), __builtin_amdgcn_alignbit(v[2], v[1], 16),
+                         __builtin_amdgcn_alignbit(v[3], v[2], 16), v[3] >> 16}
+                : v;
+    v = by >= 8u ? none : v;
+  }
+}
+template <bool kTiny = true, bool kWhole = false>
+__device__ __forceinline__ u32x4v row_get8(const uint16_t* row, uint32_t col, uint32_t cols) {
+  u32x4v v = row_load8<false, kTiny>(row, col, cols);
+  row_mend8<kTiny, kWhole>(v, col, cols);
+  return v;
+}
+template <bool kStream = false, bool kWhole = false>
+__device__ __forceinline__ void row_store8(uint16_t* row, uint32_t col, uint32_t cols, u32x4v v) {
+  if (kWhole ? col < cols : col + 8u <= cols) {
+    if constexpr (kStream) __builtin_nontemporal_store(v, reinterpret_cast<u32x4a2*>(row + col));
+    else *reinterpret_cast<u32x4a2*>(row + col) = v;
+  } else if constexpr (!kWhole) {
 #pragma unroll
     for (uint32_t i = 0; i < 7u; i++)
       if (col + i < cols) row[col + i] = uint16_t(v[i >> 1] >> (16u * (i & 1u)));
   }
 }
+// Loads before this are issued before it: the compiler else sinks them to their
+// uses, one after the other.
+__device__ __forceinline__ void loads_first() { __builtin_amdgcn_sched_barrier(0); }
 
-__device__ __forceinline__ float wave_sum(float v) {
+// What v holds is not known from here on, so that it is unpacked again where it
+// is used again, and not kept unpacked in twice the registers.
+__device__ __forceinline__ void keep_packed(u32x4v& v) {
 #pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
-  return v;
+  for (int i = 0; i < 4; i++) asm volatile("" : "+v"(v[i]));
 }
 
-// The sum over the kT threads of a row.  With more than one wave a row the
-// workgroup is the row: `part` holds a word a wave and is free again when the
-// next barrier is passed.
-template <uint32_t kT>
-__device__ __forceinline__ float row_sum(float v, float* part) {
-  v = wave_sum(v);
-  if constexpr (kT > 64u) {
-    if ((threadIdx.x & 63u) == 0u) part[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = 0.0f;
+// Sums over the kT threads of a row, of kN rows at once.  With more than one
+// wave a row the workgroup is the row; `part` is free again when the next
+// barrier is passed.
+template <uint32_t kT, uint32_t kN>
+__device__ __forceinline__ void row_sums(float (&v)[kN], float (*part)[kN]) {
 #pragma unroll
-    for (uint32_t i = 0; i < kT / 64u; i++) v += part[i];
+  for (int d = int(kT < 64u ? kT : 64u) / 2; d > 0; d >>= 1)
+#pragma unroll
+    for (uint32_t n = 0; n < kN; n++) v[n] += __shfl_xor(v[n], d);
+  if constexpr (kT > 64u) {
+    if ((threadIdx.x & 63u) == 0u)
+#pragma unroll
+      for (uint32_t n = 0; n < kN; n++) part[threadIdx.x >> 6][n] = v[n];
+    __syncthreads();
+#pragma unroll
+    for (uint32_t n = 0; n < kN; n++) {
+      v[n] = 0.0f;
+#pragma unroll
+      for (uint32_t i = 0; i < kT / 64u; i++) v[n] += part[i][n];
+    }
   }
-  return v;
 }
 
 // A row takes kT threads, each kU units of 8 values, which stay in registers
 // between the sum and the result.
-template <uint32_t kT, uint32_t kU>
+template <uint32_t kT, uint32_t kU, bool kWhole>
 __global__ __launch_bounds__(kT < 256u ? 256u : kT) void k_rms_norm(NormArgs p) {
   constexpr uint32_t kB = kT < 256u ? 256u : kT;
-  __shared__ float part[kT / 64u];
+  constexpr bool kTiny = kT < 64u && !kWhole;  // the rule's shape for few columns
+  __shared__ float part[kT <= 64u ? 1u : kT / 64u][1];
   const uint32_t t = threadIdx.x % kT;
   const uint32_t row = blockIdx.x * (kB / kT) + threadIdx.x / kT;
   if (row >= p.rows) return;
   const uint16_t* x = p.x + uint64_t(row) * p.ldx;
   const uint16_t* r = p.residual ? p.residual + uint64_t(row) * p.ldr : nullptr;
-  u32x4v v[kU], a[kU];
+  u32x4v v[kU], a[kU], w[kU];
 #pragma unroll
-  for (uint32_t u = 0; u < kU; u++) v[u] = row_load8(x, (u * kT + t) * 8u, p.cols);
+  for (uint32_t u = 0; u < kU; u++) v[u] = row_load8<true, kTiny>(x, (u * kT + t) * 8u, p.cols);
   if (r) {
 #pragma unroll
-    for (uint32_t u = 0; u < kU; u++) a[u] = row_load8(r, (u * kT + t) * 8u, p.cols);
+    for (uint32_t u = 0; u < kU; u++) a[u] = row_load8<true, kTiny>(r, (u * kT + t) * 8u, p.cols);
+  }
 #pragma unroll
-    for (uint32_t u = 0; u < kU; u++)
+  for (uint32_t u = 0; u < kU; u++) w[u] = row_load8<false, kTiny>(p.w, (u * kT + t) * 8u, p.cols);
+  loads_first();
+#pragma unroll
+  for (uint32_t u = 0; u < kU; u++) {
+    row_mend8<kTiny, kWhole>(v[u], (u * kT + t) * 8u, p.cols);
+    row_mend8<kTiny, kWhole>(w[u], (u * kT + t) * 8u, p.cols);
+  }
+  if (r) {
+#pragma unroll
+    for (uint32_t u = 0; u < kU; u++) {
+      row_mend8<kTiny, kWhole>(a[u], (u * kT + t) * 8u, p.cols);
 #pragma unroll
       for (int i = 0; i < 4; i++) v[u][i] = mx_bf16x2(bf_lo(v[u][i]) + bf_lo(a[u][i]), bf_hi(v[u][i]) + bf_hi(a[u][i]));
+    }
     if (p.h) {
 #pragma unroll
-      for (uint32_t u = 0; u < kU; u++) row_store8(p.h + uint64_t(row) * p.ldh, (u * kT + t) * 8u, p.cols, v[u]);
+      for (uint32_t u = 0; u < kU; u++) row_store8<true, kWhole>(p.h + uint64_t(row) * p.ldh, (u * kT + t) * 8u, p.cols, v[u]);
     }
   }
-  float sum = 0.0f;
+  float sum[1] = {0.0f};
 #pragma unroll
   for (uint32_t u = 0; u < kU; u++)
 #pragma unroll
-    for (int i = 0; i < 4; i++) sum = fmaf(bf_lo(v[u][i]), bf_lo(v[u][i]), fmaf(bf_hi(v[u][i]), bf_hi(v[u][i]), sum));
-  sum = row_sum<kT>(sum, part);
-  const float s = 1.0f / sqrtf(sum / float(p.cols) + p.eps);
+    for (int i = 0; i < 4; i++)
+      sum[0] = fmaf(bf_lo(v[u][i]), bf_lo(v[u][i]), fmaf(bf_hi(v[u][i]), bf_hi(v[u][i]), sum[0]));
+  row_sums<kT, 1u>(sum, part);
+  const float s = 1.0f / sqrtf(sum[0] / float(p.cols) + p.eps);
   if (p.rstd && t == 0u) p.rstd[row] = s;
   const uint32_t kp = uint32_t(mx_pitch(p.cols));
 #pragma unroll
   for (uint32_t u = 0; u < kU; u++) {
     const uint32_t col = (u * kT + t) * 8u;
-    const u32x4v w = row_load8(p.w, col, p.cols);
     u32x4v y;
 #pragma unroll
-    for (int i = 0; i < 4; i++) y[i] = mx_bf16x2(bf_lo(v[u][i]) * s * bf_lo(w[i]), bf_hi(v[u][i]) * s * bf_hi(w[i]));
-    if (col >= p.cols) y = u32x4v{0u, 0u, 0u, 0u};  // 0 s is NaN where s is
-    else if (col + 8u > p.cols)
+    for (int i = 0; i < 4; i++) y[i] = mx_bf16x2(bf_lo(v[u][i]) * s * bf_lo(w[u][i]), bf_hi(v[u][i]) * s * bf_hi(w[u][i]));
+    // behind the row's end: zeros, also where s is NaN
+    if constexpr (kWhole) {
+      if (col >= p.cols) y = u32x4v{0u, 0u, 0u, 0u};
+    } else {
 #pragma unroll
-      for (uint32_t i = 1; i < 8u; i++)
-        if (col + i >= p.cols) y[i >> 1] &= (i & 1u) ? 0xFFFFu : 0u;
-    if (p.y) row_store8(p.y + uint64_t(row) * p.ldy, col, p.cols, y);
+      for (uint32_t i = 0; i < 8u; i++) y[i >> 1] &= col + i >= p.cols ? ((i & 1u) ? 0xFFFFu : 0u) : ~0u;
+    }
+    if (p.y) row_store8<true, kWhole>(p.y + uint64_t(row) * p.ldy, col, p.cols, y);
     if (p.yq && col < kp) {
       const uint32_t sb = mx_block_scale<8>(y);
       *reinterpret_cast<u32x2v*>(p.yq + uint64_t(row) * kp + col) = mx8_codes(y, mx_scale(sb == 255u ? 127u : sb));
@@ -148,62 +210,129 @@ struct NormBackArgs {
   uint32_t dw_f32, accumulate, rows, cols, parts;
 };
 
-// A workgroup of kB threads takes every parts-th group of kB / kT rows and
-// keeps the weights and its sums of dw in registers.
-template <uint32_t kT, uint32_t kU, uint32_t kB>
-__global__ __launch_bounds__(kB) void k_rms_norm_back(NormBackArgs p) {
-  constexpr uint32_t kRows = kB / kT;
-  __shared__ float part[2][kT / 64u];
-  __shared__ float fold[kRows > 1u ? kRows * kT * 8u : 1u];
+// A workgroup takes every parts-th stretch of kB / kT * kN rows, a thread's
+// loads of kN rows at once, and keeps its sums of dw in registers.
+template <uint32_t kT, uint32_t kU, uint32_t kN, bool kWhole>
+__global__ __launch_bounds__(kT < 256u ? 256u : kT) void k_rms_norm_back(NormBackArgs p) {
+  constexpr uint32_t kB = kT < 256u ? 256u : kT, kSubs = kB / kT;
+  constexpr bool kTiny = kT < 64u && !kWhole;
+  constexpr bool kAgain = kU > 2u;  // rows that long are read again (from L2) for dx and dw: registers
+  __shared__ float part[2][kT <= 64u ? 1u : kT / 64u][kN];
+  __shared__ float fold[kSubs > 1u ? kB * 8u : 1u];
   const uint32_t t = threadIdx.x % kT, sub = threadIdx.x / kT;
+  const u32x4v none = {0u, 0u, 0u, 0u};
   float dw[kU][8];
-  u32x4v w[kU];
 #pragma unroll
-  for (uint32_t u = 0; u < kU; u++) {
-    w[u] = row_load8(p.w, (u * kT + t) * 8u, p.cols);
+  for (uint32_t u = 0; u < kU; u++)
 #pragma unroll
     for (int i = 0; i < 8; i++) dw[u][i] = 0.0f;
+  const auto weight = [&](uint32_t u) { return row_get8<kTiny, kWhole>(p.w, (u * kT + t) * 8u, p.cols); };
+  u32x4v w[kAgain ? 1 : kU];
+  if constexpr (!kAgain) {
+#pragma unroll
+    for (uint32_t u = 0; u < kU; u++) w[u] = weight(u);
   }
   uint32_t turn = 0u;
-  for (uint32_t row = blockIdx.x * kRows + sub; row - sub < p.rows; row += p.parts * kRows, turn ^= 1u) {
-    if (kRows > 1u && row >= p.rows) break;
-    u32x4v h[kU], d[kU];
-#pragma unroll
-    for (uint32_t u = 0; u < kU; u++) h[u] = row_load8(p.h + uint64_t(row) * p.ldh, (u * kT + t) * 8u, p.cols);
-#pragma unroll
-    for (uint32_t u = 0; u < kU; u++) d[u] = row_load8(p.dy + uint64_t(row) * p.lddy, (u * kT + t) * 8u, p.cols);
-    const float s = p.rstd[row];
-    float dot = 0.0f;
-#pragma unroll
-    for (uint32_t u = 0; u < kU; u++)
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const float u0 = bf_lo(h[u][i]) * s, u1 = bf_hi(h[u][i]) * s;
-        const float d0 = bf_lo(d[u][i]), d1 = bf_hi(d[u][i]);
-        dot = fmaf(d0 * bf_lo(w[u][i]), u0, fmaf(d1 * bf_hi(w[u][i]), u1, dot));
-        dw[u][2 * i] = fmaf(d0, u0, dw[u][2 * i]);
-        dw[u][2 * i + 1] = fmaf(d1, u1, dw[u][2 * i + 1]);
-      }
-    if (!p.dx) continue;
-    const float m = row_sum<kT>(dot, part[turn]) / float(p.cols);
-#pragma unroll
-    for (uint32_t u = 0; u < kU; u++) {
+  for (uint32_t first = blockIdx.x * (kSubs * kN); first < p.rows; first += p.parts * (kSubs * kN), turn ^= 1u) {
+    // rows behind the last are read as the last, and count nothing
+    const auto row_of = [&](uint32_t n) { return uint64_t(min(first + n * kSubs + sub, p.rows - 1u)); };
+    const auto live = [&](uint32_t n) { return first + n * kSubs + sub < p.rows; };
+    u32x4v h[kN][kAgain ? 1 : kU], d[kN][kAgain ? 1 : kU], e[kN][kAgain ? 1 : kU];
+    float s[kN], dot[kN];
+    const auto load = [&](uint32_t n, uint32_t u, uint32_t to, bool dh) {
       const uint32_t col = (u * kT + t) * 8u;
-      u32x4v e = {0u, 0u, 0u, 0u}, o;
-      if (p.dh) e = row_load8(p.dh + uint64_t(row) * p.lddh, col, p.cols);
+      h[n][to] = row_load8<!kAgain, kTiny>(p.h + row_of(n) * p.ldh, col, p.cols);
+      d[n][to] = row_load8<!kAgain, kTiny>(p.dy + row_of(n) * p.lddy, col, p.cols);
+      if (dh && p.dh) e[n][to] = row_load8<true, kTiny>(p.dh + row_of(n) * p.lddh, col, p.cols);
+    };
+    const auto mend = [&](uint32_t n, uint32_t u, uint32_t to, bool dh) {
+      const uint32_t col = (u * kT + t) * 8u;
+      row_mend8<kTiny, kWhole>(h[n][to], col, p.cols);
+      row_mend8<kTiny, kWhole>(d[n][to], col, p.cols);
+      if (dh && p.dh) row_mend8<kTiny, kWhole>(e[n][to], col, p.cols);
+      h[n][to] = live(n) ? h[n][to] : none;
+      d[n][to] = live(n) ? d[n][to] : none;
+    };
+    // dot += sum of dy w h s, and dw += dy h s
+    const auto sums = [&](uint32_t n, uint32_t u, uint32_t at, u32x4v wu, bool dots, bool dws) {
 #pragma unroll
       for (int i = 0; i < 4; i++) {
-        const float g0 = bf_lo(d[u][i]) * bf_lo(w[u][i]), g1 = bf_hi(d[u][i]) * bf_hi(w[u][i]);
-        o[i] = mx_bf16x2(fmaf(s, g0 - bf_lo(h[u][i]) * s * m, bf_lo(e[i])), fmaf(s, g1 - bf_hi(h[u][i]) * s * m, bf_hi(e[i])));
+        const float u0 = bf_lo(h[n][at][i]) * s[n], u1 = bf_hi(h[n][at][i]) * s[n];
+        const float d0 = bf_lo(d[n][at][i]), d1 = bf_hi(d[n][at][i]);
+        if (dots) dot[n] = fmaf(d0 * bf_lo(wu[i]), u0, fmaf(d1 * bf_hi(wu[i]), u1, dot[n]));
+        if (dws) {
+          dw[u][2 * i] = fmaf(d0, u0, dw[u][2 * i]);
+          dw[u][2 * i + 1] = fmaf(d1, u1, dw[u][2 * i + 1]);
+        }
       }
-      row_store8(p.dx + uint64_t(row) * p.lddx, col, p.cols, o);
+      loads_first();
+    };
+    const auto out = [&](uint32_t n, uint32_t u, uint32_t at, u32x4v wu, float m) {
+      u32x4v o;
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const float g0 = bf_lo(d[n][at][i]) * bf_lo(wu[i]), g1 = bf_hi(d[n][at][i]) * bf_hi(wu[i]);
+        const float e0 = p.dh ? bf_lo(e[n][at][i]) : 0.0f, e1 = p.dh ? bf_hi(e[n][at][i]) : 0.0f;
+        o[i] = mx_bf16x2(fmaf(s[n], g0 - bf_lo(h[n][at][i]) * s[n] * m, e0), fmaf(s[n], g1 - bf_hi(h[n][at][i]) * s[n] * m, e1));
+      }
+      if (live(n)) row_store8<true, kWhole>(p.dx + row_of(n) * p.lddx, (u * kT + t) * 8u, p.cols, o);
+      loads_first();
+    };
+#pragma unroll
+    for (uint32_t n = 0; n < kN; n++) {
+      s[n] = live(n) ? p.rstd[row_of(n)] : 0.0f;
+      dot[n] = 0.0f;
+    }
+    if constexpr (kAgain) {
+      static_assert(kN == 1u, "one row");
+      if (p.dx) {
+#pragma unroll
+        for (uint32_t u = 0; u < kU; u++) {
+          load(0u, u, 0u, false);
+          mend(0u, u, 0u, false);
+          sums(0u, u, 0u, weight(u), true, false);
+        }
+        row_sums<kT, kN>(dot, part[turn]);
+      }
+      const float m = dot[0] / float(p.cols);
+#pragma unroll
+      for (uint32_t u = 0; u < kU; u++) {
+        const u32x4v wu = weight(u);
+        load(0u, u, 0u, true);
+        mend(0u, u, 0u, true);
+        sums(0u, u, 0u, wu, false, true);
+        if (p.dx) out(0u, u, 0u, wu, m);
+      }
+    } else {
+#pragma unroll
+      for (uint32_t n = 0; n < kN; n++)
+#pragma unroll
+        for (uint32_t u = 0; u < kU; u++) load(n, u, u, true);
+      loads_first();
+#pragma unroll
+      for (uint32_t n = 0; n < kN; n++)
+#pragma unroll
+        for (uint32_t u = 0; u < kU; u++) {
+          mend(n, u, u, true);
+          sums(n, u, u, w[u], true, true);
+          keep_packed(h[n][u]);
+          keep_packed(d[n][u]);
+        }
+      if (!p.dx) continue;
+      row_sums<kT, kN>(dot, part[turn]);
+#pragma unroll
+      for (uint32_t n = 0; n < kN; n++) {
+        const float m = dot[n] / float(p.cols);
+#pragma unroll
+        for (uint32_t u = 0; u < kU; u++) out(n, u, u, w[u], m);
+      }
     }
   }
   if (!p.dw) return;
   float* to = p.sums + uint64_t(blockIdx.x) * p.cols;
 #pragma unroll
   for (uint32_t u = 0; u < kU; u++) {
-    if constexpr (kRows > 1u) {
+    if constexpr (kSubs > 1u) {
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < 8; i++) fold[(sub * 8u + i) * kT + t] = dw[u][i];
@@ -211,7 +340,7 @@ __global__ __launch_bounds__(kB) void k_rms_norm_back(NormBackArgs p) {
       for (uint32_t i = threadIdx.x; i < kT * 8u; i += kB) {
         float v = 0.0f;
 #pragma unroll
-        for (uint32_t r = 0; r < kRows; r++) v += fold[(r * 8u + i % 8u) * kT + i / 8u];
+        for (uint32_t r = 0; r < kSubs; r++) v += fold[(r * 8u + i % 8u) * kT + i / 8u];
         const uint32_t col = u * kT * 8u + i;
         if (col < p.cols) to[col] = v;
       }
@@ -224,22 +353,22 @@ __global__ __launch_bounds__(kB) void k_rms_norm_back(NormBackArgs p) {
   }
 }
 
-// dw: the workgroups' sums added in order, 64 columns a workgroup, every
-// sixteenth of the rows of sums a wave.
+// dw: the workgroups' sums added in order, 32 columns a workgroup, every 32nd
+// of the rows of sums to each of its 32 rows of threads.
 __global__ __launch_bounds__(1024) void k_rms_norm_join(NormBackArgs p) {
-  __shared__ float part[16][64];
-  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
-  const uint32_t col = blockIdx.x * 64u + lane;
+  __shared__ float part[32][32];
+  const uint32_t c = threadIdx.x & 31u, r = threadIdx.x >> 5;
+  const uint32_t col = blockIdx.x * 32u + c;
   float v = 0.0f;
   if (col < p.cols) {
-#pragma unroll 8
-    for (uint32_t i = wave; i < p.parts; i += 16u) v += p.sums[uint64_t(i) * p.cols + col];
+#pragma unroll 16
+    for (uint32_t i = r; i < p.parts; i += 32u) v += p.sums[uint64_t(i) * p.cols + col];
   }
-  part[wave][lane] = v;
+  part[r][c] = v;
   __syncthreads();
-  if (wave || col >= p.cols) return;
+  if (r || col >= p.cols) return;
 #pragma unroll
-  for (uint32_t i = 1; i < 16u; i++) v += part[i][lane];
+  for (uint32_t i = 1; i < 32u; i++) v += part[i][c];
   if (p.dw_f32) {
     float* o = static_cast<float*>(p.dw) + col;
     *o = p.accumulate ? *o + v : v;
@@ -250,7 +379,7 @@ __global__ __launch_bounds__(1024) void k_rms_norm_join(NormBackArgs p) {
 }
 
 // Rows a workgroup of the backward pass takes at once, and how many workgroups.
-uint32_t norm_back_rows(uint32_t cols) { return cols <= 2048u ? 8u : 1u; }
+uint32_t norm_back_rows(uint32_t cols) { return cols <= 128u ? 64u : cols <= 512u ? 16u : cols <= 4096u ? 4u : 1u; }
 uint32_t norm_back_parts(uint64_t rows, uint32_t cols) {
   const uint64_t groups = cdiv(rows, norm_back_rows(cols));
   return uint32_t(groups < kNormParts ? groups : kNormParts);
@@ -293,13 +422,21 @@ ciera_status rms_norm(const void* d_x, uint64_t ldx, const void* d_residual, uin
   p.eps = eps;
   p.rows = uint32_t(rows);
   p.cols = uint32_t(cols);
-  const uint64_t grid = cols <= 2048u ? cdiv(rows, 4u) : rows;
-  if (grid > (cols <= 8192u ? kMxMostGroups : 0xFFFFFFFFull / 1024u)) return CIERA_ERR_ARG;
-  (void)hipGetLastError();
-  if (cols <= 2048u) launch(k_rms_norm<64u, 4u>, dim3(uint32_t(grid)), dim3(256), stream, p);
-  else if (cols <= 8192u) launch(k_rms_norm<256u, 4u>, dim3(uint32_t(grid)), dim3(256), stream, p);
-  else launch(k_rms_norm<1024u, 4u>, dim3(uint32_t(grid)), dim3(1024), stream, p);
-  return launch_status();
+  const auto go = [&](auto threads, auto units) {
+    constexpr uint32_t kT = decltype(threads)::value, kU = decltype(units)::value, kB = kT < 256u ? 256u : kT;
+    const uint64_t grid = cdiv(rows, kB / kT);
+    if (grid > 0xFFFFFFFFull / kB) return CIERA_ERR_ARG;
+    (void)hipGetLastError();
+    if (cols % 8u == 0u) launch(k_rms_norm<kT, kU, true>, dim3(uint32_t(grid)), dim3(kB), stream, p);
+    else launch(k_rms_norm<kT, kU, false>, dim3(uint32_t(grid)), dim3(kB), stream, p);
+    return launch_status();
+  };
+  if (cols <= 128u) return go(Num<16u>(), Num<1u>());
+  if (cols <= 512u) return go(Num<64u>(), Num<1u>());
+  if (cols <= 2048u) return go(Num<256u>(), Num<1u>());
+  if (cols <= 4096u) return go(Num<256u>(), Num<2u>());
+  if (cols <= 8192u) return go(Num<256u>(), Num<4u>());
+  return go(Num<1024u>(), Num<4u>());
 }
 
 uint64_t rms_norm_workspace_size(uint64_t rows, uint64_t cols) {
@@ -347,13 +484,22 @@ ciera_status rms_norm_backward(const void* d_dy, uint64_t lddy, const void* d_h,
   p.parts = norm_back_parts(rows, uint32_t(cols));
   (void)hipGetLastError();
   if (rows) {
-    if (cols <= 2048u) launch(k_rms_norm_back<64u, 4u, 512u>, dim3(p.parts), dim3(512), stream, p);
-    else if (cols <= 8192u) launch(k_rms_norm_back<256u, 4u, 256u>, dim3(p.parts), dim3(256), stream, p);
-    else launch(k_rms_norm_back<1024u, 4u, 1024u>, dim3(p.parts), dim3(1024), stream, p);
+    const auto go = [&](auto threads, auto units, auto rows_at_once) {
+      constexpr uint32_t kT = decltype(threads)::value, kU = decltype(units)::value, kN = decltype(rows_at_once)::value;
+      const dim3 grid(p.parts), block(kT < 256u ? 256u : kT);
+      if (cols % 8u == 0u) launch(k_rms_norm_back<kT, kU, kN, true>, grid, block, stream, p);
+      else launch(k_rms_norm_back<kT, kU, kN, false>, grid, block, stream, p);
+    };
+    if (cols <= 128u) go(Num<16u>(), Num<1u>(), Num<4u>());
+    else if (cols <= 512u) go(Num<64u>(), Num<1u>(), Num<4u>());
+    else if (cols <= 2048u) go(Num<256u>(), Num<1u>(), Num<4u>());
+    else if (cols <= 4096u) go(Num<512u>(), Num<1u>(), Num<4u>());
+    else if (cols <= 8192u) go(Num<512u>(), Num<2u>(), Num<1u>());
+    else go(Num<1024u>(), Num<4u>(), Num<1u>());
     st = launch_status();
     if (st != CIERA_OK) return st;
   }
-  if (d_dw) launch(k_rms_norm_join, dim3(uint32_t(cdiv(cols, 64u))), dim3(1024), stream, p);
+  if (d_dw) launch(k_rms_norm_join, dim3(uint32_t(cdiv(cols, 32u))), dim3(1024), stream, p);
   return launch_status();
 }
 
