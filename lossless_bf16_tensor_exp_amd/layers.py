@@ -23,23 +23,23 @@ import ctypes
 
 import torch
 
-from . import load_library
-from .mx import _BF16, _bytes, _call, _f32, _i64, _rows
+from . import _raise, load_library
+from .mx import _BF16, _current_device, _f32, _i64, _raw_stream, _rows, _u8
 
 _i32 = torch.int32
 _vp, _u64, _u32, _int = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint32, ctypes.c_int
-_bound = False
+_functions = {}
 
 
 def _bind():
-    global _bound
-    lib = load_library()
-    if not _bound:
-        for name, args in {"rms_norm_workspace_size": [_u64] * 2, "expert_workspace_size": [_u64, _u64, _u32],
-                           "low_rank_workspace_size": [_u64] * 4 + [_u32]}.items():
-            getattr(lib, name).argtypes, getattr(lib, name).restype = args, _u64
+    """The C functions by name."""
+    if not _functions:
+        lib = load_library()
         m = [_vp, _u64]  # a matrix and its row stride, or a buffer and its length
         sigs = {
+            "rms_norm_workspace_size": [_u64] * 2,
+            "expert_workspace_size": [_u64, _u64, _u32],
+            "low_rank_workspace_size": [_u64] * 4 + [_u32],
             "rms_norm": m + m + [_vp, ctypes.c_float] + m + m + m + [_vp, _u64, _u64, _vp],
             "rms_norm_backward": m + m + [_vp, _vp] + m + m + [_vp, _u32, _u32, _u64, _u64] + m + [_vp],
             "expert_sort": [_vp, _u32, _u64, _u64, _u32, _vp, _vp, _vp] + m + [_vp],
@@ -49,50 +49,92 @@ def _bind():
             "low_rank_add": m + [_vp] * 5 + m + [_u32] + m + [_u32] + [_u64] * 4 + [_u32] + m + [_vp],
         }
         for name, args in sigs.items():
-            getattr(lib, name).argtypes, getattr(lib, name).restype = args, _int
-        _bound = True
-    return lib
+            f = getattr(lib, name)
+            f.argtypes, f.restype = args, _u64 if name.endswith("_size") else _int
+            _functions[name] = f
+    return _functions
 
 
-def _matrix(t, name, rows, cols, f32=False):
+def _elsewhere(t, name, device):
+    raise ValueError(f"{name} is on {t.device}" + (f", the call's first tensor on cuda:{device}" if device >= 0 else ""))
+
+
+def _matrix(t, name, device, rows, cols, f32=False):
     """Address and row stride of a matrix of rows x cols; none for None."""
     if t is None:
         return None, 0
-    r, c, ld = _rows(t, name, f32)
-    if r != rows or c != cols:
-        raise ValueError(f"{name} is {r} x {c}, not {rows} x {cols}")
+    dtype = t.dtype
+    if dtype not in _BF16 and not (f32 and dtype is _f32):
+        _rows(t, name, f32)  # says what is wrong
+    if t.get_device() != device or device < 0:
+        _elsewhere(t, name, device)
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} is {tuple(t.shape)}, not {(rows, cols)}")
+    ld, step = t.stride()
+    if rows <= 1:
+        ld = cols
+    if (step != 1 and cols > 1) or ld < cols:
+        raise ValueError(f"{name}'s rows must be contiguous and must not overlap")
     return t.data_ptr(), ld
 
 
-def _vector(t, name, dtypes, shape):
+def _vector(t, name, device, dtypes, shape):
     """Address of a contiguous tensor of a type and shape; none for None."""
     if t is None:
         return None
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must hold {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be a contiguous device tensor {shape}, got {tuple(t.shape)}")
+    if t.get_device() != device or device < 0:
+        _elsewhere(t, name, device)
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous device tensor {tuple(shape)}, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _buffer(t, name):
-    return (None, 0) if t is None else _bytes(t, name)
+def _buffer(t, name, device):
+    """Address and length of a buffer of bytes; none for None."""
+    if t is None:
+        return None, 0
+    if t.dtype is not _u8 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous uint8 device tensor")
+    if t.get_device() != device or device < 0:
+        _elsewhere(t, name, device)
+    n = t.numel()
+    return (t.data_ptr() if n else None), n
 
 
-def _tensors(*given):
-    return [t for t in given if t is not None]
+def _entries(t, name, device, dtypes):
+    """Tokens, choices and address of a table of entries; one dimension: one choice a token."""
+    shape = t.shape
+    if len(shape) not in (1, 2):
+        raise ValueError(f"{name} must be (tokens, choices) or (tokens,), got {tuple(shape)}")
+    return shape[0], shape[1] if len(shape) == 2 else 1, _vector(t, name, device, dtypes, shape)
+
+
+def _call(name, device, stream, *args):
+    """The C call ``name`` on the tensors' device: the current stream there
+    unless one is given."""
+    f = _functions[name]
+    s = _raw_stream(device) if stream is None else stream.cuda_stream
+    if device == _current_device():
+        st = f(*args, s)
+    else:
+        with torch.cuda.device(device):
+            st = f(*args, s)
+    if st:
+        _raise(st, name)
 
 
 def rms_norm_workspace_size(rows: int, cols: int) -> int:
-    return _bind().rms_norm_workspace_size(rows, cols)
+    return _bind()["rms_norm_workspace_size"](rows, cols)
 
 
 def expert_workspace_size(tokens: int, choices: int, experts: int) -> int:
-    return _bind().expert_workspace_size(tokens, choices, experts)
+    return _bind()["expert_workspace_size"](tokens, choices, experts)
 
 
 def low_rank_workspace_size(tokens: int, n: int, k: int, rank: int, adapters: int) -> int:
-    return _bind().low_rank_workspace_size(tokens, n, k, rank, adapters)
+    return _bind()["low_rank_workspace_size"](tokens, n, k, rank, adapters)
 
 
 def rms_norm(x, weight, y=None, yq=None, residual=None, h=None, rstd=None, eps: float = 1e-6, stream=None) -> None:
@@ -102,10 +144,10 @@ def rms_norm(x, weight, y=None, yq=None, residual=None, h=None, rstd=None, eps: 
     are what the backward pass takes."""
     _bind()
     rows, cols, ldx = _rows(x, "x")
-    _call("rms_norm", x.get_device(), _tensors(weight, y, yq, residual, h, rstd), stream, x.data_ptr(), ldx,
-          *_matrix(residual, "residual", rows, cols), _vector(weight, "weight", _BF16, (cols,)), eps,
-          *_matrix(h, "h", rows, cols), *_matrix(y, "y", rows, cols), *_buffer(yq, "yq"),
-          _vector(rstd, "rstd", (_f32,), (rows,)), rows, cols)
+    on = x.get_device()
+    _call("rms_norm", on, stream, x.data_ptr(), ldx, *_matrix(residual, "residual", on, rows, cols),
+          _vector(weight, "weight", on, _BF16, (cols,)), eps, *_matrix(h, "h", on, rows, cols),
+          *_matrix(y, "y", on, rows, cols), *_buffer(yq, "yq", on), _vector(rstd, "rstd", on, (_f32,), (rows,)), rows, cols)
 
 
 def rms_norm_backward(dy, h, weight, rstd, dx, dw, ws=None, dh=None, accumulate: bool = False, stream=None) -> None:
@@ -115,18 +157,12 @@ def rms_norm_backward(dy, h, weight, rstd, dx, dw, ws=None, dh=None, accumulate:
     ``dw`` needs the workspace.  ``h`` is x where there was no residual."""
     _bind()
     rows, cols, lddy = _rows(dy, "dy")
-    _call("rms_norm_backward", dy.get_device(), _tensors(h, weight, rstd, dx, dw, ws, dh), stream, dy.data_ptr(), lddy,
-          *_matrix(h, "h", rows, cols), _vector(weight, "weight", _BF16, (cols,)), _vector(rstd, "rstd", (_f32,), (rows,)),
-          *_matrix(dh, "dh", rows, cols), *_matrix(dx, "dx", rows, cols), _vector(dw, "dw", (*_BF16, _f32), (cols,)),
-          1 if dw is not None and dw.dtype is _f32 else 0, 1 if accumulate else 0, rows, cols, *_buffer(ws, "ws"))
-
-
-def _entries(t, name, dtypes):
-    """Tokens, choices and address of a table of entries; one dimension: one choice a token."""
-    if t.dim() not in (1, 2):
-        raise ValueError(f"{name} must be (tokens, choices) or (tokens,), got {tuple(t.shape)}")
-    shape = tuple(t.shape)
-    return shape[0], shape[1] if len(shape) == 2 else 1, _vector(t, name, dtypes, shape)
+    on = dy.get_device()
+    _call("rms_norm_backward", on, stream, dy.data_ptr(), lddy, *_matrix(h, "h", on, rows, cols),
+          _vector(weight, "weight", on, _BF16, (cols,)), _vector(rstd, "rstd", on, (_f32,), (rows,)),
+          *_matrix(dh, "dh", on, rows, cols), *_matrix(dx, "dx", on, rows, cols),
+          _vector(dw, "dw", on, (*_BF16, _f32), (cols,)), 1 if dw is not None and dw.dtype is _f32 else 0,
+          1 if accumulate else 0, rows, cols, *_buffer(ws, "ws", on))
 
 
 def expert_sort(ids, offsets, place, order, ws, stream=None) -> None:
@@ -135,14 +171,14 @@ def expert_sort(ids, offsets, place, order, ws, stream=None) -> None:
     the products take; ``place`` (as ids, int32) is each entry's row; ``order``
     (all entries, int32, or None) each row's entry."""
     _bind()
-    tokens, choices, at = _entries(ids, "ids", (_i32, _i64))
+    on = ids.get_device()
+    tokens, choices, at = _entries(ids, "ids", on, (_i32, _i64))
     if offsets.dim() != 1 or offsets.numel() < 2:
         raise ValueError("offsets must hold experts + 1 row numbers")
     experts = offsets.numel() - 1
-    _call("expert_sort", ids.get_device(), _tensors(offsets, place, order, ws), stream, at, 1 if ids.dtype is _i64 else 0,
-          tokens, choices, experts, _vector(offsets, "offsets", (_i64,), (experts + 1,)),
-          _vector(place, "place", (_i32,), tuple(ids.shape)), _vector(order, "order", (_i32,), (tokens * choices,)),
-          *_bytes(ws, "ws"))
+    _call("expert_sort", on, stream, at, 1 if ids.dtype is _i64 else 0, tokens, choices, experts,
+          _vector(offsets, "offsets", on, (_i64,), (experts + 1,)), _vector(place, "place", on, (_i32,), ids.shape),
+          _vector(order, "order", on, (_i32,), (tokens * choices,)), *_buffer(ws, "ws", on))
 
 
 def expert_dispatch(x, place, out=None, outq=None, rows=None, stream=None) -> None:
@@ -151,13 +187,14 @@ def expert_dispatch(x, place, out=None, outq=None, rows=None, stream=None) -> No
     given)."""
     _bind()
     n, cols, ldx = _rows(x, "x")
-    tokens, choices, at = _entries(place, "place", (_i32,))
+    on = x.get_device()
+    tokens, choices, at = _entries(place, "place", on, (_i32,))
     if n != tokens:
         raise ValueError(f"{n} rows of x and {tokens} of place")
     if rows is None:
         rows = out.shape[0] if out is not None else tokens * choices
-    _call("expert_dispatch", x.get_device(), _tensors(place, out, outq), stream, x.data_ptr(), ldx, at, tokens, choices,
-          cols, rows, *_matrix(out, "out", rows, cols), *_buffer(outq, "outq"))
+    _call("expert_dispatch", on, stream, x.data_ptr(), ldx, at, tokens, choices, cols, rows,
+          *_matrix(out, "out", on, rows, cols), *_buffer(outq, "outq", on))
 
 
 def expert_combine(rows, place, out, weights=None, residual=None, stream=None) -> None:
@@ -167,11 +204,11 @@ def expert_combine(rows, place, out, weights=None, residual=None, stream=None) -
     the gradient of expert_dispatch."""
     _bind()
     n, cols, ld = _rows(rows, "rows", True)
-    tokens, choices, at = _entries(place, "place", (_i32,))
-    _call("expert_combine", rows.get_device(), _tensors(place, out, weights, residual), stream, rows.data_ptr(), ld,
-          1 if rows.dtype is _f32 else 0, n, at, _vector(weights, "weights", (_f32,), tuple(place.shape)),
-          *_matrix(residual, "residual", tokens, cols), *_matrix(out, "out", tokens, cols, True),
-          1 if out.dtype is _f32 else 0, tokens, choices, cols)
+    on = rows.get_device()
+    tokens, choices, at = _entries(place, "place", on, (_i32,))
+    _call("expert_combine", on, stream, rows.data_ptr(), ld, 1 if rows.dtype is _f32 else 0, n, at,
+          _vector(weights, "weights", on, (_f32,), place.shape), *_matrix(residual, "residual", on, tokens, cols),
+          *_matrix(out, "out", on, tokens, cols, True), 1 if out.dtype is _f32 else 0, tokens, choices, cols)
 
 
 def expert_combine_backward(dout, rows, place, drows, dweights, weights=None, stream=None) -> None:
@@ -180,12 +217,12 @@ def expert_combine_backward(dout, rows, place, drows, dweights, weights=None, st
     may be None."""
     _bind()
     n, cols, ld = _rows(rows, "rows", True)
-    tokens, choices, at = _entries(place, "place", (_i32,))
-    shape = tuple(place.shape)
-    _call("expert_combine_backward", dout.get_device(), _tensors(rows, place, drows, dweights, weights), stream,
-          *_matrix(dout, "dout", tokens, cols), rows.data_ptr(), ld, 1 if rows.dtype is _f32 else 0, n, at,
-          _vector(weights, "weights", (_f32,), shape), *_matrix(drows, "drows", n, cols),
-          _vector(dweights, "dweights", (_f32,), shape), tokens, choices, cols)
+    on = rows.get_device()
+    tokens, choices, at = _entries(place, "place", on, (_i32,))
+    shape = place.shape
+    _call("expert_combine_backward", on, stream, *_matrix(dout, "dout", on, tokens, cols), rows.data_ptr(), ld,
+          1 if rows.dtype is _f32 else 0, n, at, _vector(weights, "weights", on, (_f32,), shape),
+          *_matrix(drows, "drows", on, n, cols), _vector(dweights, "dweights", on, (_f32,), shape), tokens, choices, cols)
 
 
 def low_rank_add(x, a, b, offsets, y, ws, base=None, order=None, scales=None, stream=None) -> None:
@@ -196,12 +233,13 @@ def low_rank_add(x, a, b, offsets, y, ws, base=None, order=None, scales=None, st
     rows lie sorted) are expert_sort's; rows of no adapter are base."""
     _bind()
     tokens, k, ldx = _rows(x, "x")
+    on = x.get_device()
     if a.dim() != 3 or b.dim() != 3:
         raise ValueError("a must be (adapters, rank, k) and b (adapters, n, rank)")
-    adapters, rank, n = a.shape[0], a.shape[1], b.shape[1]
-    ap, bp = _vector(a, "a", _BF16, (adapters, rank, k)), _vector(b, "b", _BF16, (adapters, n, rank))
-    _call("low_rank_add", x.get_device(), _tensors(a, b, offsets, y, ws, base, order, scales), stream, x.data_ptr(), ldx,
-          ap, bp, _vector(scales, "scales", (_f32,), (adapters,)), _vector(offsets, "offsets", (_i64,), (adapters + 1,)),
-          _vector(order, "order", (_i32,), (tokens,)), *_matrix(base, "base", tokens, n, True),
-          1 if base is not None and base.dtype is _f32 else 0, *_matrix(y, "y", tokens, n, True),
-          1 if y.dtype is _f32 else 0, tokens, n, k, rank, adapters, *_bytes(ws, "ws"))
+    (adapters, rank, _), n = a.shape, b.shape[1]
+    _call("low_rank_add", on, stream, x.data_ptr(), ldx, _vector(a, "a", on, _BF16, (adapters, rank, k)),
+          _vector(b, "b", on, _BF16, (adapters, n, rank)), _vector(scales, "scales", on, (_f32,), (adapters,)),
+          _vector(offsets, "offsets", on, (_i64,), (adapters + 1,)), _vector(order, "order", on, (_i32,), (tokens,)),
+          *_matrix(base, "base", on, tokens, n, True), 1 if base is not None and base.dtype is _f32 else 0,
+          *_matrix(y, "y", on, tokens, n, True), 1 if y.dtype is _f32 else 0, tokens, n, k, rank, adapters,
+          *_buffer(ws, "ws", on))

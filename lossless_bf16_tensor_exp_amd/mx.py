@@ -38,7 +38,8 @@ _f32, _i64, _u8 = torch.float32, torch.int64, torch.uint8
 _vp, _u64, _u32, _i32 = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint32, ctypes.c_int
 _SCALED = 4  # CIERA_MX_SCALED
 _bound = None
-_current_device = torch.cuda.current_device
+# the current device without the check that the GPU is initialised (a device tensor was there first; 0.2 us a call)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 # the current stream's handle without the Stream object around it (1 us a call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 

@@ -15,8 +15,9 @@ BIG = 1 << 40
 
 @pytest.fixture(scope="module")
 def lib():
-    from lossless_bf16_tensor_exp_amd import layers
-    return layers._bind()
+    from lossless_bf16_tensor_exp_amd import layers, load_library
+    layers._bind()
+    return load_library()
 
 
 def norm(lib, x=P, ldx=64, r=None, w=P, eps=1e-6, h=None, y=P, yq=None, size=BIG, rstd=None, rows=4, cols=64):
