@@ -290,6 +290,8 @@ struct LowRankOuter {
     if constexpr (kF32) return __uint_as_float(base[r][i]);
     else return i & 1u ? bf_hi(base[r][i >> 1]) : bf_lo(base[r][i >> 1]);
   }
+  // past the last-level cache (16,384 rows at rank 16: 45 us instead of 48; rows of no adapter 24
+  // instead of 35)
   __device__ __forceinline__ void store(const LowRankArgs& p, uint32_t c, const v4f (&sum)[4], bool add) {
     const uint32_t col = c + (threadIdx.x & 15u) * 4u;
 #pragma unroll
@@ -302,7 +304,7 @@ struct LowRankOuter {
       if (p.y_f32) {
         float* o = static_cast<float*>(p.y) + to;
         if (col + 4u <= p.n) {
-          *reinterpret_cast<v4fa4*>(o) = v4f{v[0], v[1], v[2], v[3]};
+          __builtin_nontemporal_store(v4f{v[0], v[1], v[2], v[3]}, reinterpret_cast<v4fa4*>(o));
         } else {
 #pragma unroll
           for (uint32_t i = 0; i < 3u; i++)
@@ -311,7 +313,7 @@ struct LowRankOuter {
       } else {
         uint16_t* o = static_cast<uint16_t*>(p.y) + to;
         if (col + 4u <= p.n) {
-          *reinterpret_cast<u32x2a2*>(o) = u32x2v{mx_bf16x2(v[0], v[1]), mx_bf16x2(v[2], v[3])};
+          __builtin_nontemporal_store(u32x2v{mx_bf16x2(v[0], v[1]), mx_bf16x2(v[2], v[3])}, reinterpret_cast<u32x2a2*>(o));
         } else {
 #pragma unroll
           for (uint32_t i = 0; i < 3u; i++)
