@@ -1,6 +1,7 @@
 """Buffer owners for the C ABI: allocate the stream, workspace, size slot and
 exponent caches once with torch, then call the library on them.  ``MxLinear``
-does the same for a linear layer on microscaled matrices.
+does the same for a linear layer on microscaled matrices; ``RmsNorm``,
+``ExpertRows`` and ``LowRankAdapters`` for what stands around its products.
 
 Allocation happens only in the constructors; ``encode``/``decode`` only pass
 pointers.
@@ -10,9 +11,11 @@ from __future__ import annotations
 import torch
 
 from . import (CieraError, ciera_decode, ciera_encode, ciera_encode_e0, ciera_encode_spec, ciera_max_encoded_size,
-               ciera_read_error, ciera_workspace_size, mx4_encode, mx4_encoded_size, mx4_matmul, mx4_matmul_dx,
-               mx4_matmul_mx8, mx8_encode, mx8_encoded_size, mx8_wgrad, mx_workspace_size, zip3_decode, zip3_encode,
-               zip3_encode_e0, zip3_encode_spec, zip3_max_encoded_size, zip3_workspace_size)
+               ciera_read_error, ciera_workspace_size, expert_combine, expert_combine_backward, expert_dispatch,
+               expert_sort, expert_workspace_size, low_rank_add, low_rank_workspace_size, mx4_encode, mx4_encoded_size,
+               mx4_matmul, mx4_matmul_dx, mx4_matmul_mx8, mx8_encode, mx8_encoded_size, mx8_wgrad, mx_workspace_size,
+               rms_norm, rms_norm_backward, rms_norm_workspace_size, zip3_decode, zip3_encode, zip3_encode_e0,
+               zip3_encode_spec, zip3_max_encoded_size, zip3_workspace_size)
 
 
 class Zip3Codec:
@@ -165,6 +168,22 @@ class MxLinear:
                        self.scaled and y.dtype is not torch.float32)
         self.kept = x.shape[0]
 
+    def keep_dispatched(self, x, experts: "ExpertRows", y, stream=None):
+        """``keep`` of the rows that ``experts`` makes of the tokens x: they go
+        right into the checkpoint.  y has a row for every entry of the sort;
+        ``backward`` takes ``experts.offsets``."""
+        rows = experts.rows()
+        if rows > self.tokens:
+            raise ValueError(f"{rows} rows in a layer made for {self.tokens}")
+        self._shape("x", x, (experts.tokens(), self.k))
+        self._shape("y", y, (rows, self.n))
+        self._table(experts.offsets)
+        self.kept = None
+        expert_dispatch(x, experts.place, outq=self.xq, rows=rows, stream=stream)
+        mx4_matmul_mx8(self.xq, self.k, self.w, y, self.ws, experts.offsets, stream,
+                       self.scaled and y.dtype is not torch.float32)
+        self.kept = rows
+
     def backward(self, dy, dx, dw, offsets=None, accumulate: bool = False, stream=None):
         """dx = dy W and dw = dy^T x from the checkpoint that ``keep`` left;
         either output may be None."""
@@ -187,6 +206,140 @@ class MxLinear:
         """Status of the last product (CIERA_ERR_ARG for offsets that are not
         in order); synchronises."""
         return ciera_read_error(self.ws, stream)
+
+
+class RmsNorm:
+    """y = h w / sqrt(mean(h^2) + eps), h = x + residual, of up to ``rows`` rows
+    of ``cols``; keeps the weight, what the backward pass needs of a call's rows
+    (``rstd``) and its workspace.  ``forward`` and the ``backward`` that belongs
+    to it are on one stream, or ordered by the caller; autograd records
+    neither."""
+
+    def __init__(self, rows: int, cols: int, eps: float = 1e-6, device="cuda"):
+        size = rms_norm_workspace_size(rows, cols)
+        if size == 0:
+            raise ValueError(f"no norm of {rows} x {cols}")
+        self.rows, self.cols, self.eps = rows, cols, eps
+        self.weight = torch.ones(cols, dtype=torch.bfloat16, device=device)
+        self.rstd = torch.empty(rows, dtype=torch.float32, device=device)
+        self.ws = torch.empty(size, dtype=torch.uint8, device=device)
+        self.kept = None  # rows of the last forward pass
+
+    def forward(self, x, y=None, yq=None, residual=None, h=None, stream=None):
+        """y in BF16, in mx8 (yq), or both; h where a residual is given."""
+        rows = x.shape[0]
+        if rows > self.rows:
+            raise ValueError(f"{rows} rows in a norm made for {self.rows}")
+        rms_norm(x, self.weight, y, yq, residual, h, self.rstd[:rows], self.eps, stream)
+        self.kept = rows
+
+    def backward(self, dy, h, dx, dw, dh=None, accumulate: bool = False, stream=None):
+        """dx and dw of the last forward pass, h being what it left there (x
+        without a residual), and dh the gradient that h has from elsewhere."""
+        if dy.shape[0] != self.kept:
+            raise ValueError(f"{dy.shape[0]} rows of dy for " +
+                             ("no forward pass" if self.kept is None else f"a forward pass of {self.kept}"))
+        rms_norm_backward(dy, h, self.weight, self.rstd[:self.kept], dx, dw, self.ws, dh, accumulate, stream)
+
+
+class ExpertRows:
+    """The rows of up to ``tokens`` tokens, ``choices`` entries each, by expert:
+    ``sort`` keeps the entries' rows (``place``), the rows' entries (``order``)
+    and the experts' ``offsets``, which the products take; the other calls move
+    rows by them.  A sort and the calls that use it belong to one stream, or are
+    ordered by the caller."""
+
+    def __init__(self, tokens: int, choices: int, experts: int, device="cuda"):
+        size = expert_workspace_size(tokens, choices, experts)
+        if size == 0:
+            raise ValueError(f"no sort of {tokens} x {choices} by {experts} experts")
+        self.most, self.choices, self.experts = tokens, choices, experts
+        self.offsets = torch.zeros(experts + 1, dtype=torch.int64, device=device)
+        self._place = torch.empty(tokens, choices, dtype=torch.int32, device=device)
+        self._order = torch.empty(tokens * choices, dtype=torch.int32, device=device)
+        self.ws = torch.empty(size, dtype=torch.uint8, device=device)
+        self.place, self.order = self._place[:0], self._order[:0]
+
+    def tokens(self) -> int:
+        return self.place.shape[0]
+
+    def rows(self) -> int:
+        """Entries of the last sort: rows that a buffer of dispatched rows has,
+        the last ones unused where entries have no expert."""
+        return self.order.shape[0]
+
+    def sort(self, ids, stream=None):
+        """ids (tokens, choices) int32 or int64, -1 for no expert."""
+        if ids.dim() != 2 or ids.shape[1] != self.choices or ids.shape[0] > self.most:
+            raise ValueError(f"ids are {tuple(ids.shape)}, the sort was made for {(self.most, self.choices)}")
+        tokens = ids.shape[0]
+        place, order = self._place[:tokens], self._order[:tokens * self.choices]
+        expert_sort(ids, self.offsets, place, order, self.ws, stream)
+        self.place, self.order = place, order
+
+    def dispatch(self, x, out=None, outq=None, stream=None):
+        """Each token's row to its entries' rows, in BF16 or mx8."""
+        expert_dispatch(x, self.place, out, outq, self.rows() if out is None else None, stream)
+
+    def dispatch_backward(self, drows, dx, stream=None):
+        """dx = the sum of a token's entries' gradients."""
+        expert_combine(drows, self.place, dx, stream=stream)
+
+    def combine(self, rows, out, weights=None, residual=None, stream=None):
+        """out = residual + a token's rows by its weights."""
+        expert_combine(rows, self.place, out, weights, residual, stream)
+
+    def combine_backward(self, dout, rows, drows, dweights, weights=None, stream=None):
+        expert_combine_backward(dout, rows, self.place, drows, dweights, weights, stream)
+
+    def error(self, stream=None) -> int:
+        """Status of the last sort (CIERA_ERR_ARG for a number of no expert);
+        synchronises."""
+        return ciera_read_error(self.ws, stream)
+
+
+class LowRankAdapters:
+    """``adapters`` low-rank adapters, B (n, rank) and A (rank, k) each, beside a
+    projection that all requests share: y = base + scale B (A x) by the adapter
+    of each of up to ``tokens`` rows.  ``plan`` sorts a step's rows once for all
+    its projections (another adapters' plan of the same rows can be given to
+    ``add``); rows of adapter -1 are base.  For serving: there is no gradient."""
+
+    def __init__(self, tokens: int, n: int, k: int, rank: int, adapters: int, device="cuda"):
+        size = low_rank_workspace_size(tokens, n, k, rank, adapters)
+        if size == 0:
+            raise ValueError(f"no adapters of rank {rank} for {tokens} x {n} x {k}")
+        self.n, self.k, self.rank, self.adapters = n, k, rank, adapters
+        self.a = torch.zeros(adapters, rank, k, dtype=torch.bfloat16, device=device)
+        self.b = torch.zeros(adapters, n, rank, dtype=torch.bfloat16, device=device)
+        self.scales = torch.ones(adapters, dtype=torch.float32, device=device)
+        self.rows = ExpertRows(tokens, 1, adapters, device)
+        self.ws = torch.empty(size, dtype=torch.uint8, device=device)
+
+    def load(self, index: int, a, b, scale: float = 1.0):
+        """Adapter ``index``: a (r, k) and b (n, r), r at most the rank."""
+        r = a.shape[0]
+        if r > self.rank or tuple(a.shape) != (r, self.k) or tuple(b.shape) != (self.n, r):
+            raise ValueError(f"a is {tuple(a.shape)} and b {tuple(b.shape)}, the adapters' are of rank {self.rank} for "
+                             f"{self.n} x {self.k}")
+        self.a[index].zero_()
+        self.b[index].zero_()
+        self.a[index, :r] = a
+        self.b[index, :, :r] = b
+        self.scales[index] = scale
+
+    def plan(self, ids, stream=None):
+        """ids (tokens,) int32 or int64: each row's adapter, -1 for none."""
+        self.rows.sort(ids.view(-1, 1), stream)
+
+    def add(self, x, y, base=None, plan: "LowRankAdapters | None" = None, stream=None):
+        """y = base + the adapters' part; base may be y, or None for zeros."""
+        rows = (self if plan is None else plan).rows
+        low_rank_add(x, self.a, self.b, rows.offsets, y, self.ws, base, rows.order, self.scales, stream)
+
+    def error(self, stream=None) -> int:
+        """Status of the last ``plan``, and of the last ``add``; synchronises."""
+        return ciera_read_error(self.rows.ws, stream) or ciera_read_error(self.ws, stream)
 
 
 # One-shot calls: allocate the stream and workspace with torch, run one
