@@ -196,8 +196,9 @@ __global__ __launch_bounds__(1024) void k_expert_sort(SortArgs p) {
 }
 
 // ---------------------------------------------------------------------------
-// The rows.  A token takes 1 << lt threads, each a unit of 8 values or several
-// that far apart; a workgroup of 256 holds 256 >> lt tokens.
+// The rows.  A token takes 1 << lt threads, each a unit of 8 values; a workgroup
+// of 256 holds 256 >> lt tokens.  Rows longer than a workgroup go on in the
+// grid's second dimension (backward, which sums over a row: in a loop).
 // ---------------------------------------------------------------------------
 struct RowArgs {
   const uint16_t* x;  // dispatch: the tokens; backward: dout
@@ -233,8 +234,8 @@ __global__ __launch_bounds__(256) void k_dispatch(RowArgs p) {
   const uint16_t* x = p.x + uint64_t(token) * p.ldx;
   const int32_t* place = p.place + uint64_t(token) * p.choices;
   const uint32_t kp = uint32_t(mx_pitch(p.cols));
-  const uint32_t end = p.q ? kp : p.cols;
-  for (uint32_t col = t * 8u; col < end; col += 8u << p.lt) {
+  const uint32_t col = (blockIdx.y << p.lt | t) * 8u;
+  if (col < (p.q ? kp : p.cols)) {
     const u32x4v v = row_get8<!kWave>(x, col, p.cols);
     u32x2v codes = {0u, 0u};
     uint32_t sb = 0u;
@@ -309,7 +310,8 @@ __global__ __launch_bounds__(256) void k_combine(RowArgs p) {
   if (token >= p.tokens) return;
   const int32_t* place = p.place + uint64_t(token) * p.choices;
   const float* weights = p.weights ? p.weights + uint64_t(token) * p.choices : nullptr;
-  for (uint32_t col = t * 8u; col < p.cols; col += 8u << p.lt) {
+  const uint32_t col = (blockIdx.y << p.lt | t) * 8u;
+  if (col < p.cols) {
     float sum[8];
     Row8<false, !kWave> r;
     if (p.residual) r.load(p.residual, uint64_t(token) * p.ldr, col, p.cols);
@@ -449,9 +451,9 @@ ciera_status row_common(RowArgs& p, const int32_t* d_place, uint64_t tokens, uin
   p.cols = uint32_t(cols);
   p.slots = uint32_t(slots);
   p.lt = row_threads(cols);
-  return cdiv(tokens, 256u >> p.lt) > kMxMostGroups ? CIERA_ERR_ARG : CIERA_OK;
+  return cdiv(tokens, 256u >> p.lt) * cdiv(mx_pitch(cols), 8u << p.lt) > kMxMostGroups ? CIERA_ERR_ARG : CIERA_OK;
 }
-dim3 row_grid(const RowArgs& p) { return dim3(uint32_t(cdiv(p.tokens, 256u >> p.lt))); }
+dim3 row_grid(const RowArgs& p, uint64_t cols) { return dim3(uint32_t(cdiv(p.tokens, 256u >> p.lt)), uint32_t(cdiv(cols, 8u << p.lt))); }
 
 }  // namespace
 
@@ -516,8 +518,9 @@ ciera_status expert_dispatch(const void* d_x, uint64_t ldx, const int32_t* d_pla
   p.q = static_cast<uint8_t*>(d_outq);
   p.qs = p.q ? p.q + mx_scales_at(rows, cols, 8u) : nullptr;
   (void)hipGetLastError();
-  if (p.lt >= 6u) launch(k_dispatch<true>, row_grid(p), dim3(256), stream, p);
-  else launch(k_dispatch<false>, row_grid(p), dim3(256), stream, p);
+  const dim3 grid = row_grid(p, p.q ? mx_pitch(cols) : cols);
+  if (p.lt >= 6u) launch(k_dispatch<true>, grid, dim3(256), stream, p);
+  else launch(k_dispatch<false>, grid, dim3(256), stream, p);
   return launch_status();
 }
 
@@ -542,11 +545,11 @@ ciera_status expert_combine(const void* d_rows, uint64_t ldrows, uint32_t rows_f
   p.out_f32 = out_f32;
   (void)hipGetLastError();
   if (p.lt >= 6u) {
-    if (rows_f32) launch(k_combine<true, true>, row_grid(p), dim3(256), stream, p);
-    else launch(k_combine<true, false>, row_grid(p), dim3(256), stream, p);
+    if (rows_f32) launch(k_combine<true, true>, row_grid(p, cols), dim3(256), stream, p);
+    else launch(k_combine<true, false>, row_grid(p, cols), dim3(256), stream, p);
   } else {
-    if (rows_f32) launch(k_combine<false, true>, row_grid(p), dim3(256), stream, p);
-    else launch(k_combine<false, false>, row_grid(p), dim3(256), stream, p);
+    if (rows_f32) launch(k_combine<false, true>, row_grid(p, cols), dim3(256), stream, p);
+    else launch(k_combine<false, false>, row_grid(p, cols), dim3(256), stream, p);
   }
   return launch_status();
 }
@@ -574,11 +577,11 @@ ciera_status expert_combine_backward(const void* d_dout, uint64_t lddout, const 
   p.dweights = d_dweights;
   (void)hipGetLastError();
   if (p.lt >= 6u) {
-    if (rows_f32) launch(k_combine_back<true, true>, row_grid(p), dim3(256), stream, p);
-    else launch(k_combine_back<true, false>, row_grid(p), dim3(256), stream, p);
+    if (rows_f32) launch(k_combine_back<true, true>, row_grid(p, 1u), dim3(256), stream, p);
+    else launch(k_combine_back<true, false>, row_grid(p, 1u), dim3(256), stream, p);
   } else {
-    if (rows_f32) launch(k_combine_back<false, true>, row_grid(p), dim3(256), stream, p);
-    else launch(k_combine_back<false, false>, row_grid(p), dim3(256), stream, p);
+    if (rows_f32) launch(k_combine_back<false, true>, row_grid(p, 1u), dim3(256), stream, p);
+    else launch(k_combine_back<false, false>, row_grid(p, 1u), dim3(256), stream, p);
   }
   return launch_status();
 }

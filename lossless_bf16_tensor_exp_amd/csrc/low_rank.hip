@@ -292,13 +292,13 @@ struct LowRankOuter {
   }
   // past the last-level cache (16,384 rows at rank 16: 45 us instead of 48; rows of no adapter 24
   // instead of 35)
-  __device__ __forceinline__ void store(const LowRankArgs& p, uint32_t c, const v4f (&sum)[4], bool add) {
+  __device__ __forceinline__ void store(const LowRankArgs& p, uint32_t c, const v4f (&sum)[4]) {
     const uint32_t col = c + (threadIdx.x & 15u) * 4u;
 #pragma unroll
     for (uint32_t r = 0; r < 4u; r++) {
       float v[4];
 #pragma unroll
-      for (uint32_t f = 0; f < 4u; f++) v[f] = add ? value(p, r, f) + sum[f][r] : value(p, r, f);
+      for (uint32_t f = 0; f < 4u; f++) v[f] = value(p, r, f) + sum[f][r];
       if (!live[r]) continue;
       const uint64_t to = row[r] * p.ldy + col;
       if (p.y_f32) {
@@ -320,14 +320,6 @@ struct LowRankOuter {
             if (col + i < p.n) o[i] = mx_bf16(v[i]);
         }
       }
-    }
-  }
-  // rows of no adapter: base alone
-  __device__ __forceinline__ void bare(const LowRankArgs& p, uint32_t c, uint32_t n1) {
-    const v4f none[4] = {};
-    for (; c < n1; c += 64u) {
-      load_base(p, c);
-      store(p, c, none, false);
     }
   }
   // columns c .. n1 - 1, B and base of the first 64 being loaded
@@ -366,11 +358,53 @@ struct LowRankOuter {
         }
         wave_lds();
       }
-      store(p, c, sum, true);
+      store(p, c, sum);
       if (c + 64u < n1) load_base(p, c + 64u);
     }
   }
 };
+
+// Rows of no adapter: base alone.  Two rows a wave, its lanes side by side, the
+// loads of four units of 8 values together.
+template <bool kF32>
+__device__ __forceinline__ void low_rank_bare(const LowRankArgs& p, uint32_t row0, uint32_t row1, uint32_t c, uint32_t n1) {
+  static_assert(kLowRankThreads / 64u * 2u == kLowRankRows, "two rows a wave");
+  const uint32_t lane = threadIdx.x & 63u;
+  for (uint32_t r = 0; r < 2u; r++) {
+    uint32_t row;
+    if (!low_rank_row(p, row0, row1, mx_first(threadIdx.x >> 6) * 2u + r, row)) continue;
+    for (uint32_t at = c + lane * 8u; at < n1; at += 4u * 512u) {
+      Row8<kF32> v[4];
+      if (p.base) {
+#pragma unroll
+        for (uint32_t i = 0; i < 4u; i++) v[i].load(p.base, uint64_t(row) * p.ldb, at + i * 512u, p.n);
+        loads_first();
+      }
+#pragma unroll
+      for (uint32_t i = 0; i < 4u; i++) {
+        const uint32_t col = at + i * 512u;
+        if (col >= n1) break;
+        if (p.base) v[i].mend(col, p.n);
+        float e[8];
+#pragma unroll
+        for (int k = 0; k < 8; k++) e[k] = p.base ? v[i].value(k) : 0.0f;
+        const uint64_t to = uint64_t(row) * p.ldy;
+        if (!p.y_f32) {
+          row_store8<true>(static_cast<uint16_t*>(p.y) + to, col, p.n,
+                           u32x4v{mx_bf16x2(e[0], e[1]), mx_bf16x2(e[2], e[3]), mx_bf16x2(e[4], e[5]), mx_bf16x2(e[6], e[7])});
+        } else if (col + 8u <= p.n) {
+          float* o = static_cast<float*>(p.y) + to + col;
+          __builtin_nontemporal_store(v4f{e[0], e[1], e[2], e[3]}, reinterpret_cast<v4fa4*>(o));
+          __builtin_nontemporal_store(v4f{e[4], e[5], e[6], e[7]}, reinterpret_cast<v4fa4*>(o + 4));
+        } else {
+#pragma unroll
+          for (uint32_t k = 0; k < 7u; k++)
+            if (col + k < p.n) static_cast<float*>(p.y)[to + col + k] = e[k];
+        }
+      }
+    }
+  }
+}
 
 // kF: fragments of 16 ranks (1, 2, 4 or 8).
 template <uint32_t kF, bool kF32>
@@ -390,15 +424,13 @@ __global__ __launch_bounds__(kLowRankThreads) void k_low_rank(LowRankArgs p) {
   if (blockIdx.x == 0u) low_rank_report(p);
   uint32_t g, row0, row1, slab;
   if (!low_rank_tile(p, g, row0, row1, slab)) return;
+  if (g >= p.adapters) {  // no adapter
+    if (p.base != p.y) low_rank_bare<kF32>(p, row0, row1, slab * p.slab, min(p.n, (slab + 1u) * p.slab));
+    return;
+  }
   uint32_t c, n1;
   low_rank_share<kW>(wave, slab * p.slab, min(p.n, (slab + 1u) * p.slab), c, n1);
   Outer o;
-  if (g >= p.adapters) {  // no adapter
-    if (p.base == p.y) return;
-    o.rows(p, 0u, row0, row1);
-    o.bare(p, c, n1);
-    return;
-  }
   Inner in;
   in.rows(p, g, row0, row1);
   v4f acc[kF];

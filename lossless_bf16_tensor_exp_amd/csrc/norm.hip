@@ -101,8 +101,8 @@ __device__ __forceinline__ void keep_packed(u32x4v& v) {
 }
 
 // Sums over the kT threads of a row, of kN rows at once.  With more than one
-// wave a row the workgroup is the row; `part` is free again when the next
-// barrier is passed.
+// wave a row, `part` has a line for each wave of the workgroup and is free again
+// when the next barrier is passed, which every thread of it has to reach.
 template <uint32_t kT, uint32_t kN>
 __device__ __forceinline__ void row_sums(float (&v)[kN], float (*part)[kN]) {
 #pragma unroll
@@ -118,7 +118,7 @@ __device__ __forceinline__ void row_sums(float (&v)[kN], float (*part)[kN]) {
     for (uint32_t n = 0; n < kN; n++) {
       v[n] = 0.0f;
 #pragma unroll
-      for (uint32_t i = 0; i < kT / 64u; i++) v[n] += part[i][n];
+      for (uint32_t i = 0; i < kT / 64u; i++) v[n] += part[threadIdx.x / kT * (kT / 64u) + i][n];
     }
   }
 }
@@ -129,10 +129,12 @@ template <uint32_t kT, uint32_t kU, bool kWhole>
 __global__ __launch_bounds__(kT < 256u ? 256u : kT) void k_rms_norm(NormArgs p) {
   constexpr uint32_t kB = kT < 256u ? 256u : kT;
   constexpr bool kTiny = kT < 64u && !kWhole;  // the rule's shape for few columns
-  __shared__ float part[kT <= 64u ? 1u : kT / 64u][1];
+  __shared__ float part[kT <= 64u ? 1u : kB / 64u][1];
   const uint32_t t = threadIdx.x % kT;
-  const uint32_t row = blockIdx.x * (kB / kT) + threadIdx.x / kT;
-  if (row >= p.rows) return;
+  const uint32_t at = blockIdx.x * (kB / kT) + threadIdx.x / kT;
+  const uint32_t row = min(at, p.rows - 1u);  // rows behind the last: for the barrier alone
+  const bool live = at < p.rows;
+  if (kT <= 64u && !live) return;
   const uint16_t* x = p.x + uint64_t(row) * p.ldx;
   const uint16_t* r = p.residual ? p.residual + uint64_t(row) * p.ldr : nullptr;
   u32x4v v[kU], a[kU], w[kU];
@@ -157,7 +159,7 @@ __global__ __launch_bounds__(kT < 256u ? 256u : kT) void k_rms_norm(NormArgs p) 
 #pragma unroll
       for (int i = 0; i < 4; i++) v[u][i] = mx_bf16x2(bf_lo(v[u][i]) + bf_lo(a[u][i]), bf_hi(v[u][i]) + bf_hi(a[u][i]));
     }
-    if (p.h) {
+    if (p.h && live) {
 #pragma unroll
       for (uint32_t u = 0; u < kU; u++) row_store8<true, kWhole>(p.h + uint64_t(row) * p.ldh, (u * kT + t) * 8u, p.cols, v[u]);
     }
@@ -169,6 +171,7 @@ __global__ __launch_bounds__(kT < 256u ? 256u : kT) void k_rms_norm(NormArgs p) 
     for (int i = 0; i < 4; i++)
       sum[0] = fmaf(bf_lo(v[u][i]), bf_lo(v[u][i]), fmaf(bf_hi(v[u][i]), bf_hi(v[u][i]), sum[0]));
   row_sums<kT, 1u>(sum, part);
+  if (!live) return;
   const float s = 1.0f / sqrtf(sum[0] / float(p.cols) + p.eps);
   if (p.rstd && t == 0u) p.rstd[row] = s;
   const uint32_t kp = uint32_t(mx_pitch(p.cols));
@@ -217,7 +220,7 @@ __global__ __launch_bounds__(kT < 256u ? 256u : kT) void k_rms_norm_back(NormBac
   constexpr uint32_t kB = kT < 256u ? 256u : kT, kSubs = kB / kT;
   constexpr bool kTiny = kT < 64u && !kWhole;
   constexpr bool kAgain = kU > 2u;  // rows that long are read again (from L2) for dx and dw: registers
-  __shared__ float part[2][kT <= 64u ? 1u : kT / 64u][kN];
+  __shared__ float part[2][kT <= 64u ? 1u : kB / 64u][kN];
   __shared__ float fold[kSubs > 1u ? kB * 8u : 1u];
   const uint32_t t = threadIdx.x % kT, sub = threadIdx.x / kT;
   const u32x4v none = {0u, 0u, 0u, 0u};
@@ -379,7 +382,9 @@ __global__ __launch_bounds__(1024) void k_rms_norm_join(NormBackArgs p) {
 }
 
 // Rows a workgroup of the backward pass takes at once, and how many workgroups.
-uint32_t norm_back_rows(uint32_t cols) { return cols <= 128u ? 64u : cols <= 512u ? 16u : cols <= 4096u ? 4u : 1u; }
+uint32_t norm_back_rows(uint32_t cols) {
+  return cols <= 32u ? 256u : cols <= 128u ? 64u : cols <= 512u ? 16u : cols <= 1024u ? 8u : cols <= 2048u ? 4u : cols <= 4096u ? 2u : 1u;
+}
 uint32_t norm_back_parts(uint64_t rows, uint32_t cols) {
   const uint64_t groups = cdiv(rows, norm_back_rows(cols));
   return uint32_t(groups < kNormParts ? groups : kNormParts);
@@ -431,8 +436,10 @@ ciera_status rms_norm(const void* d_x, uint64_t ldx, const void* d_residual, uin
     else launch(k_rms_norm<kT, kU, false>, dim3(uint32_t(grid)), dim3(kB), stream, p);
     return launch_status();
   };
+  if (cols <= 32u && !d_yq) return go(Num<4u>(), Num<1u>());  // a row of mx8 is 16 units long
   if (cols <= 128u) return go(Num<16u>(), Num<1u>());
   if (cols <= 512u) return go(Num<64u>(), Num<1u>());
+  if (cols <= 1024u) return go(Num<128u>(), Num<1u>());
   if (cols <= 2048u) return go(Num<256u>(), Num<1u>());
   if (cols <= 4096u) return go(Num<256u>(), Num<2u>());
   if (cols <= 8192u) return go(Num<256u>(), Num<4u>());
@@ -490,10 +497,12 @@ ciera_status rms_norm_backward(const void* d_dy, uint64_t lddy, const void* d_h,
       if (cols % 8u == 0u) launch(k_rms_norm_back<kT, kU, kN, true>, grid, block, stream, p);
       else launch(k_rms_norm_back<kT, kU, kN, false>, grid, block, stream, p);
     };
-    if (cols <= 128u) go(Num<16u>(), Num<1u>(), Num<4u>());
+    if (cols <= 32u) go(Num<4u>(), Num<1u>(), Num<4u>());
+    else if (cols <= 128u) go(Num<16u>(), Num<1u>(), Num<4u>());
     else if (cols <= 512u) go(Num<64u>(), Num<1u>(), Num<4u>());
+    else if (cols <= 1024u) go(Num<128u>(), Num<1u>(), Num<4u>());
     else if (cols <= 2048u) go(Num<256u>(), Num<1u>(), Num<4u>());
-    else if (cols <= 4096u) go(Num<512u>(), Num<1u>(), Num<4u>());
+    else if (cols <= 4096u) go(Num<256u>(), Num<2u>(), Num<2u>());
     else if (cols <= 8192u) go(Num<512u>(), Num<2u>(), Num<1u>());
     else go(Num<1024u>(), Num<4u>(), Num<1u>());
     st = launch_status();
