@@ -124,7 +124,12 @@ __device__ __forceinline__ void row_sums(float (&v)[kN], float (*part)[kN]) {
 }
 
 // A row takes kT threads, each kU units of 8 values, which stay in registers
-// between the sum and the result.
+// between the sum and the result: memory is read and written once, and bounds
+// it.  16,384 x 2,048 with a residual, h, y and yq, 302 MB: 50 us, 6.0 TB/s.  All
+// but the weight and yq goes past the last-level cache, which keeps yq for its
+// reader (55 us through it).  As many threads as a row has units: 65,536 rows of
+// 64 with a wave each 79 us, with 16 threads 10; 30,000 of 1,021 with 256 threads
+// 69 us, with 128 48.
 template <uint32_t kT, uint32_t kU, bool kWhole>
 __global__ __launch_bounds__(kT < 256u ? 256u : kT) void k_rms_norm(NormArgs p) {
   constexpr uint32_t kB = kT < 256u ? 256u : kT;
@@ -214,7 +219,12 @@ struct NormBackArgs {
 };
 
 // A workgroup takes every parts-th stretch of kB / kT * kN rows, a thread's
-// loads of kN rows at once, and keeps its sums of dw in registers.
+// loads of kN rows at once (with one barrier for their sums), and keeps its sums
+// of dw in registers to the end.  Bound by memory: 16,384 x 2,048 with dh, 268
+// MB: 48 us, 5.6 TB/s (53 through the last-level cache), and 4 for the sums of
+// dw, 512 workgroups' (768: 59 and 4.5; 256: 66 and 4).  Registers leave two
+// waves a SIMD, whose 48 KB in flight a CU are enough.  Two rows of 4,096 with 256
+// threads: 8,000 of them 53 us; four with 512 threads 64.
 template <uint32_t kT, uint32_t kU, uint32_t kN, bool kWhole>
 __global__ __launch_bounds__(kT < 256u ? 256u : kT) void k_rms_norm_back(NormBackArgs p) {
   constexpr uint32_t kB = kT < 256u ? 256u : kT, kSubs = kB / kT;
@@ -357,7 +367,8 @@ __global__ __launch_bounds__(kT < 256u ? 256u : kT) void k_rms_norm_back(NormBac
 }
 
 // dw: the workgroups' sums added in order, 32 columns a workgroup, every 32nd
-// of the rows of sums to each of its 32 rows of threads.
+// of the rows of sums to each of its 32 rows of threads, so that a thread waits
+// for memory once or twice.  Bound by its launch (4 us).
 __global__ __launch_bounds__(1024) void k_rms_norm_join(NormBackArgs p) {
   __shared__ float part[32][32];
   const uint32_t c = threadIdx.x & 31u, r = threadIdx.x >> 5;
