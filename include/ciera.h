@@ -1,7 +1,7 @@
 /*
- * ciera.h -- C ABI of the lossless BF16 codec for MI355X (gfx950), and of
- * the matrices in 8 and 4 bits and their products ("Microscaled matrices"
- * below).
+ * ciera.h -- C ABI of the lossless BF16 codec for MI355X (gfx950), of the
+ * matrices in 8 and 4 bits and their products ("Microscaled matrices" below),
+ * and of what stands around those products in a layer.
  *
  * The codec turns a BF16 tensor into a byte stream and back, bit for bit:
  *
@@ -342,8 +342,9 @@ ciera_status ciera_encode_spec(const void* d_x, uint64_t n, uint32_t B, uint8_t*
  * forces the planner; its decode one; the single-read encode two; the rANS
  * encode three and its decode one; the speculative encode seven on a tensor
  * of more than 16 chunks, whatever the hint; the batch decode one; the mx
- * calls one each, or two where a gradient's contraction goes in parts) each
- * take the next pair, which the HIP runtime records at that kernel's start and end
+ * calls one each, or two where a gradient's contraction goes in parts;
+ * rms_norm_backward two with d_dw, expert_sort one or two, the other calls
+ * around the products one) each take the next pair, which the HIP runtime records at that kernel's start and end
  * (hipExtLaunchKernel);
  * hipEventElapsedTime then gives the kernel's own duration.  The handles are
  * copied; a later call replaces the queue, n_pairs = 0 clears it.  Returns
