@@ -553,7 +553,7 @@ ciera_status mx8_wgrad(const void* d_dy, uint64_t lddy, const void* d_xq, uint64
  *   d_dw        out  cols BF16 (dw_f32 = 0) or FP32 (1), or null; accumulate =
  *                    1 adds to it (one rounding of the sum)
  *   d_ws        tmp  ws_bytes >= rms_norm_workspace_size(rows, cols); needed
- *                    for d_dw only; holds no status for ciera_read_error */
+ *                    and written for d_dw only */
 ciera_status rms_norm(const void* d_x, uint64_t ldx, const void* d_residual, uint64_t ldr, const void* d_w, float eps,
                       void* d_h, uint64_t ldh, void* d_y, uint64_t ldy, void* d_yq, uint64_t yq_bytes, float* d_rstd,
                       uint64_t rows, uint64_t cols, hipStream_t stream);

@@ -284,6 +284,78 @@ def test_fewer_tokens_than_the_owners_were_made_for():
         lu.within(dw, want.cpu(), room.cpu(), U)
 
 
+@pytest.mark.gpu
+def test_no_tokens():
+    require_gpu()
+    say("a block without tokens")
+    b = Block(5, 128, 64, 2, 3)
+    b.rows.sort(torch.empty(0, 2, dtype=torch.int32, device="cuda"))
+    assert (b.rows.offsets == 0).all() and b.rows.error() == 0
+    none, u = torch.empty(0, 128, dtype=bf16, device="cuda"), torch.empty(0, 64, dtype=bf16, device="cuda")
+    b.up.load(torch.ones(3, 64, 128, dtype=bf16, device="cuda"))
+    b.up.keep_dispatched(none, b.rows, u)
+    dw = torch.full((3, 64, 128), 7.0, device="cuda")
+    b.up.backward(u, none, dw, b.rows.offsets)
+    assert b.up.error() == 0 and (dw == 0).all()
+    b.rows.combine(none, none, torch.empty(0, 2, device="cuda"))
+    # tokens, none of them with an expert
+    b.rows.sort(torch.full((5, 2), -1, dtype=torch.int32, device="cuda"))
+    x, z = torch.ones(5, 128, dtype=bf16, device="cuda"), torch.full((10, 128), float("nan"), dtype=bf16, device="cuda")
+    out, w = torch.empty_like(x), torch.full((5, 2), float("nan"), device="cuda")
+    b.rows.dispatch(x, out=z)
+    b.rows.combine(z, out, w, x)
+    assert z.isnan().all() and torch.equal(out, x)
+    b.rows.combine_backward(x, z, z, w)
+    assert z.isnan().all() and (w == 0).all()
+
+
+@pytest.mark.gpu
+def test_a_stream_of_the_caller():
+    """Every call goes to the stream it is given: behind what is queued there, whatever the current one does."""
+    require_gpu()
+    say("calls on a given stream")
+    import lossless_bf16_tensor_exp_amd as c
+    gen = torch.Generator().manual_seed(2)
+    (x, r, ids, weights, dout), _ = inputs(gen, 300, 256, 64, 2, 5)
+    x, r, ids, weights, dout = (t.cuda() for t in (x, r, ids, weights, dout))
+    a, b = torch.randn(5, 8, 256, generator=gen).to(bf16).cuda(), torch.randn(5, 256, 8, generator=gen).to(bf16).cuda()
+    w = torch.ones(256, dtype=bf16, device="cuda")
+
+    def run(x, stream):
+        def new(*shape, dtype=bf16):
+            return torch.zeros(*shape, dtype=dtype, device="cuda")
+
+        h, y, dx, rows, drows = new(300, 256), new(300, 256), new(300, 256), new(600, 256), new(600, 256)
+        s, dw, dweights, out, z = new(300, dtype=torch.float32), new(256), new(300, 2, dtype=torch.float32), new(300, 256), new(300, 256)
+        offsets, place, order = new(6, dtype=torch.int64), new(300, 2, dtype=torch.int32), new(300, dtype=torch.int32)
+        ws = [new(n, dtype=torch.uint8) for n in (c.rms_norm_workspace_size(300, 256), c.expert_workspace_size(300, 2, 5),
+                                                  c.low_rank_workspace_size(300, 256, 256, 8, 5))]
+        one = ids[:, 0].contiguous()
+        torch.cuda.synchronize()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                torch.cuda._sleep(20_000_000)  # some 10 ms: what went to another stream would read x before it is there
+                x.copy_(later)
+        c.rms_norm(x, w, y=y, residual=r, h=h, rstd=s, stream=stream)
+        c.expert_sort(ids, offsets, place, None, ws[1], stream=stream)
+        c.expert_dispatch(y, place, out=rows, stream=stream)
+        c.expert_combine(rows, place, out, weights=weights, residual=h, stream=stream)
+        c.expert_combine_backward(dout, rows, place, drows, dweights, weights=weights, stream=stream)
+        c.rms_norm_backward(out, h, w, s, dx, dw, ws[0], stream=stream)
+        c.expert_sort(one, offsets, place.view(-1)[:300], order, ws[1], stream=stream)
+        c.low_rank_add(y, a, b, offsets, z, ws[2], base=out, order=order, stream=stream)
+        status = [c.ciera_read_error(t, stream) for t in ws]
+        torch.cuda.synchronize()
+        assert status == [0, 0, 0]
+        return [h, y, dx, rows, drows, s, dw, dweights, out, z, offsets, order]
+
+    later = x.clone()
+    want = run(x, None)
+    early = torch.zeros_like(x)
+    for one, two in zip(want, run(early, torch.cuda.Stream())):
+        assert torch.equal(one, two)
+
+
 def test_owners_refuse():
     from lossless_bf16_tensor_exp_amd.codec import ExpertRows, LowRankAdapters, MxLinear, RmsNorm
     for make in (lambda: RmsNorm(4, 0, device="meta"), lambda: RmsNorm(4, 40000, device="meta"), lambda: ExpertRows(4, 0, 3, device="meta"),
