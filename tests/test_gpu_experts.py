@@ -38,7 +38,8 @@ def sort(ids, experts, order=True):
 
 @pytest.mark.parametrize("tokens,choices,experts", [(1, 1, 1), (1, 8, 64), (8, 8, 64), (63, 3, 5), (64, 1, 2), (1000, 6, 66),
                                                     (4096, 2, 128), (2500, 8, 64), (5000, 1, 4096), (300, 64, 64), (4001, 4, 1023),
-                                                    (3000, 2, 1024), (70000, 1, 3), (33000, 8, 64)])
+                                                    (3000, 2, 1024), (70000, 1, 3), (33000, 8, 64), (6143, 1, 7), (1536, 4, 7), (6145, 1, 300),
+                                                    (66000, 8, 5), (20000, 4, 4096)])
 @pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
 def test_sort(tokens, choices, experts, dtype):
     say(f"sort {tokens} x {choices} of {experts} {dtype}")

@@ -94,6 +94,22 @@ def test_whole_numbers(tokens, n, k, rank, adapters):
     assert torch.equal(y.double().cpu(), lu.low_rank(x, a, b, None, offsets, order, base)[0])
 
 
+@pytest.mark.parametrize("tokens,n,k,rank,adapters", [(3, 8200, 130, 16, 2), (20, 5000, 8200, 33, 3), (18, 3333, 5000, 128, 2),
+                                                      (9, 512, 511, 64, 8), (2000, 1100, 72, 20, 1500), (4500, 600, 64, 12, 2)])
+@pytest.mark.parametrize("y_type", [bf16, torch.float32])
+def test_slabs_and_long_contractions(tokens, n, k, rank, adapters, y_type):
+    """Few tiles, whose columns go in slabs; contractions of many steps; more lists than a wave counts at once."""
+    say(f"adapters in slabs {tokens} x {n} x {k} rank {rank} of {adapters}")
+    c = lib()
+    x, a, b, scales, offsets, order, base = case(tokens, n, k, rank, adapters)
+    y = torch.empty(tokens, n, dtype=y_type, device="cuda")
+    ws = workspace(tokens, n, k, rank, adapters)
+    c.low_rank_add(x.cuda(), a.cuda(), b.cuda(), offsets.cuda(), y, ws, base=base.cuda(), order=order.cuda(), scales=scales.cuda())
+    assert c.ciera_read_error(ws) == 0
+    want, size = lu.low_rank(x, a, b, scales, offsets, order, base)
+    lu.within(y, want, (k + 3 * rank + 4) * U * size + U * want.abs(), lu.HALF[y_type])
+
+
 def test_inner_values_keep_24_bits():
     """Inner values of 24 significant bits, picked out one by one: nothing of them is lost."""
     say("adapters, inner values whole")

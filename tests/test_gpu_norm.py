@@ -163,6 +163,32 @@ def test_backward(rows, cols, way, wider, shift, dtype):
         assert torch.equal(to, dx)
 
 
+@pytest.mark.parametrize("rows,cols", [(140000, 24), (70001, 100), (17000, 300), (9001, 520), (5003, 1408), (2100, 2056), (1100, 4100),
+                                       (1030, 8200)])
+def test_more_rows_than_go_at_once(rows, cols):
+    """Every shape with workgroups that go round more than once, the last round in part."""
+    say(f"norm backward in rounds {rows}x{cols}")
+    c = lib()
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    h, dy, dh = (torch.randn(rows, cols, generator=gen, device="cuda").to(bf16) for _ in range(3))
+    w = (1 + 0.1 * torch.randn(cols, generator=gen, device="cuda")).to(bf16)
+    y, s = torch.empty_like(h), torch.empty(rows, device="cuda")
+    c.rms_norm(h, w, y=y, rstd=s)
+    _, s64, y64 = lu.norm(h, None, w, 1e-6)
+    lu.within(s, s64.cpu(), 31 * U * s64.cpu())
+    lu.within(y, y64.cpu(), 33 * U * y64.cpu().abs(), 2.0 ** -8)
+    want, room, dw64, size = (t.cpu() for t in backward64(dy, h, w, s, dh))
+    dx, dw = torch.empty_like(h), torch.empty(cols, device="cuda")
+    ws = torch.empty(c.rms_norm_workspace_size(rows, cols), dtype=torch.uint8, device="cuda")
+    c.rms_norm_backward(dy, h, w, s, dx, dw, ws, dh=dh)
+    assert c.ciera_read_error(ws) == 0
+    lu.within(dx, want, room, 2.0 ** -8)
+    lu.within(dw, dw64, (rows + 66) * U * size, U)
+    again = torch.empty_like(dw)
+    c.rms_norm_backward(dy, h, w, s, None, again, ws)
+    assert torch.equal(again, dw)
+
+
 def test_backward_against_differences():
     """The formula itself: sum(dy y) moves by dx and dw as h and w move, in 64 bits."""
     gen = torch.Generator().manual_seed(3)
