@@ -17,8 +17,10 @@
 // What bounds it: for few rows the launch and one pass through dependent loads
 // (64 rows of 24 adapters, rank 16, k = n = 2,048: 5.9 us, of which 2.5 launch);
 // for many, memory in two phases, x and then base and y, that overlap only
-// between workgroups (16,384 rows at rank 16, 201 MB: 45 us, 4.5 TB/s; 4,001 rows
-// at rank 64, 53 MB: 17.8 us).  Base or v's loads further ahead gained nothing.
+// between workgroups (16,384 rows at rank 16, 201 MB: 45 us, 4.5 TB/s), and from
+// rank 64 on the way of A and B through LDS, once for each row tile (4,001 rows
+// at rank 64, 53 MB: 16.2 us; 16,384: 72).  Base or v's loads further ahead
+// gained nothing.
 #include "ciera.h"
 
 namespace {
@@ -158,16 +160,17 @@ __device__ __forceinline__ bool low_rank_row(const LowRankArgs& p, uint32_t row0
 }
 
 // v = A x: a wave's part of the contraction, for 16 rows.  The rows come from
-// memory as they lie, neighbouring lanes on neighbouring bytes, and go through
-// LDS into the order of the matrix instructions, whose neighbouring lanes hold
-// neighbouring rows (loaded in that order each lane's 16 bytes are a request of
-// their own: 16,384 rows, k = n = 2,048, rank 16: 60 us instead of 48; 4,001 rows at rank
-// 64: 24 instead of 18).
+// memory as they lie, neighbouring lanes on neighbouring bytes, 64 values of each
+// a step (32: more conflicts of banks; 16,384 rows, k = n = 2,048, rank 64: 83 us
+// instead of 72), and go
+// through LDS into the order of the matrix instructions, whose neighbouring
+// lanes hold neighbouring rows (loaded in that order each lane's 16 bytes are a
+// request of their own: 16,384 rows at rank 16: 60 us instead of 48).
 template <uint32_t kF>
 struct LowRankInner {
   static constexpr uint32_t kR = kF * 16u;
-  static constexpr uint32_t kStep = kF <= 2u ? 64u : 32u;  // values of k at a time
-  static constexpr uint32_t kRow = kStep * 2u;             // bytes of a row of them
+  static constexpr uint32_t kStep = 64u;        // values of k at a time
+  static constexpr uint32_t kRow = kStep * 2u;  // bytes of a row of them
   static constexpr uint32_t kChunks = kRow / 16u, kPer = 64u / kChunks;  // lanes on a row, rows a load
   static constexpr uint32_t kX = kLowRankRows / kPer, kA = kR / kPer;    // loads
   static constexpr uint32_t kLds = (kLowRankRows + kR) * kRow;
@@ -226,16 +229,17 @@ struct LowRankInner {
   }
 };
 
-// y = base + B v, 64 columns a step: B's rows through LDS likewise, 32 ranks at a
-// time.  Row 4 j + f of the 64 is column j of matrix fragment f, so that a lane
+// y = base + B v, 64 columns a step: B's rows through LDS likewise, 64 ranks at a
+// time (32: 16,384 rows at rank 64 88 us instead of 83).  Row 4 j + f of the 64 is column j of matrix fragment f, so that a lane
 // ends with four neighbouring columns of four rows, and 16 lanes with 64.  16
 // ranks fill half a matrix instruction: the other half takes v's next part.
 template <uint32_t kF, bool kF32>
 struct LowRankOuter {
   static constexpr uint32_t kR = kF * 16u;
-  static constexpr uint32_t kP = kF == 1u ? 1u : kF / 2u;  // pieces of ranks
-  static constexpr uint32_t kSteps = kF == 1u ? 2u : kP * 3u;
-  static constexpr uint32_t kRow = kF == 1u ? 32u : 64u;   // bytes of a row's piece
+  static constexpr uint32_t kRow = kF == 1u ? 32u : kF == 2u ? 64u : 128u;  // bytes of a row's piece
+  static constexpr uint32_t kP = kR * 2u / kRow;             // pieces of ranks
+  static constexpr uint32_t kHalves = kRow == 128u ? 2u : 1u;  // matrix instructions a piece and part of v
+  static constexpr uint32_t kV = kP * kHalves, kSteps = kF == 1u ? 2u : kV * 3u;
   static constexpr uint32_t kChunks = kRow / 16u, kPer = 64u / kChunks, kLoads = 64u / kPer;
   static constexpr uint32_t kFrag = 17u * kRow;            // bytes from one fragment to the next
   static constexpr uint32_t kLds = 4u * kFrag;
@@ -245,7 +249,7 @@ struct LowRankOuter {
   u32x4v w[kLoads];
   u32x4v base[4];  // BF16: the first half
   static __device__ __forceinline__ uint32_t at(uint32_t f, uint32_t j, uint32_t chunk) {
-    const uint32_t turn = kF == 1u ? j >> 3 : j >> 2;
+    const uint32_t turn = kRow == 128u ? j & 7u : kRow == 64u ? j >> 2 : j >> 3;
     return f * kFrag + j * kRow + ((chunk ^ turn) * 16u);
   }
   __device__ __forceinline__ void rows(const LowRankArgs& p, uint32_t g, uint32_t row0, uint32_t row1) {
@@ -261,7 +265,8 @@ struct LowRankOuter {
     const uint32_t lane = threadIdx.x & 63u;
 #pragma unroll
     for (uint32_t i = 0; i < kLoads; i++)
-      w[i] = row_load8(b + uint64_t(min(c + i * kPer + lane / kChunks, p.n - 1u)) * p.rank, piece * 32u + lane % kChunks * 8u, p.rank);
+      w[i] = row_load8(b + uint64_t(min(c + i * kPer + lane / kChunks, p.n - 1u)) * p.rank,
+                       piece * (kRow / 2u) + lane % kChunks * 8u, p.rank);
   }
   // this lane's four columns of its four rows: whole where none passes the end
   __device__ __forceinline__ void load_base(const LowRankArgs& p, uint32_t c) {
@@ -339,7 +344,7 @@ struct LowRankOuter {
       for (uint32_t piece = 0; piece < kP; piece++) {
         if (p.rank != kR) {
 #pragma unroll
-          for (uint32_t i = 0; i < kLoads; i++) row_mend8(w[i], piece * 32u + lane % kChunks * 8u, p.rank);
+          for (uint32_t i = 0; i < kLoads; i++) row_mend8(w[i], piece * (kRow / 2u) + lane % kChunks * 8u, p.rank);
         }
 #pragma unroll
         for (uint32_t i = 0; i < kLoads; i++) {
@@ -351,15 +356,18 @@ struct LowRankOuter {
         loads_first();
         wave_lds();
 #pragma unroll
-        for (uint32_t f = 0; f < 4u; f++) {
-          const v8bf fb = *reinterpret_cast<const v8bf*>(lds + at(f, i16, kF == 1u ? quarter & 1u : quarter));
-          if constexpr (kF == 1u) {
-            sum[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[1], fb, sum[f], 0, 0, 0);
-            sum[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[0], fb, sum[f], 0, 0, 0);
-          } else {
+        for (uint32_t h = 0; h < kHalves; h++) {
 #pragma unroll
-            for (uint32_t part = 3u; part > 0u; part--)  // the smallest part first
-              sum[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[(part - 1u) * kP + piece], fb, sum[f], 0, 0, 0);
+          for (uint32_t f = 0; f < 4u; f++) {
+            const v8bf fb = *reinterpret_cast<const v8bf*>(lds + at(f, i16, kF == 1u ? quarter & 1u : h * 4u + quarter));
+            if constexpr (kF == 1u) {
+              sum[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[1], fb, sum[f], 0, 0, 0);
+              sum[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[0], fb, sum[f], 0, 0, 0);
+            } else {
+#pragma unroll
+              for (uint32_t part = 3u; part > 0u; part--)  // the smallest part first
+                sum[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[(part - 1u) * kV + piece * kHalves + h], fb, sum[f], 0, 0, 0);
+            }
           }
         }
         wave_lds();
@@ -412,9 +420,10 @@ __device__ __forceinline__ void low_rank_bare(const LowRankArgs& p, uint32_t row
   }
 }
 
-// kF: fragments of 16 ranks (1, 2, 4 or 8).
+// kF: fragments of 16 ranks (1, 2, 4 or 8).  Registers and LDS for two workgroups
+// a CU; at 128 ranks the LDS holds one.
 template <uint32_t kF, bool kF32>
-__global__ __launch_bounds__(kLowRankThreads) void k_low_rank(LowRankArgs p) {
+__global__ __launch_bounds__(kLowRankThreads, kF <= 4u ? 4 : 2) void k_low_rank(LowRankArgs p) {
   typedef LowRankInner<kF> Inner;
   typedef LowRankOuter<kF, kF32> Outer;
   constexpr uint32_t kW = kLowRankThreads / 64u;
@@ -422,9 +431,9 @@ __global__ __launch_bounds__(kLowRankThreads) void k_low_rank(LowRankArgs p) {
   constexpr uint32_t kLine = kR + 8u;  // of a row's parts in LDS, 16 bytes more for the banks
   constexpr uint32_t kSum = kR + 4u;   // of a row's sums, likewise
   constexpr uint32_t kMine = Inner::kLds > Outer::kLds ? Inner::kLds : Outer::kLds;
-  constexpr uint32_t kSums = kW * kLowRankRows * kSum * 4u;
-  __shared__ __attribute__((aligned(256))) uint8_t lds[kW * kMine > kSums ? kW * kMine : kSums];
-  __shared__ __attribute__((aligned(16))) uint16_t parts[3][kLowRankRows][kLine];
+  constexpr uint32_t kSums = kW * kLowRankRows * kSum * 4u, kParts = 3u * kLowRankRows * kLine * 2u;
+  // sums and parts lie where the waves' tiles do before and after
+  __shared__ __attribute__((aligned(256))) uint8_t lds[kW * kMine > kSums + kParts ? kW * kMine : kSums + kParts];
   const uint32_t tid = threadIdx.x, lane = tid & 63u, i16 = lane & 15u, quarter = lane >> 4;
   const uint32_t wave = mx_first(tid >> 6);
   if (blockIdx.x == 0u) low_rank_report(p);
@@ -451,6 +460,8 @@ __global__ __launch_bounds__(kLowRankThreads) void k_low_rank(LowRankArgs p) {
   }
   __syncthreads();
   float* sums = reinterpret_cast<float*>(lds);
+  typedef uint16_t Part[kLowRankRows][kLine];
+  Part* parts = reinterpret_cast<Part*>(lds + kSums);
 #pragma unroll
   for (uint32_t f = 0; f < kF; f++)
     *reinterpret_cast<v4f*>(sums + (wave * kLowRankRows + i16) * kSum + f * 16u + quarter * 4u) = acc[f];
@@ -475,26 +486,32 @@ __global__ __launch_bounds__(kLowRankThreads) void k_low_rank(LowRankArgs p) {
       v[i] = part < 3u ? *reinterpret_cast<const v8bf*>(&parts[part][i16][(quarter & 1u) * 8u])
                        : __builtin_bit_cast(v8bf, u32x4v{0u, 0u, 0u, 0u});
     } else {
-      v[i] = *reinterpret_cast<const v8bf*>(&parts[i / Outer::kP][i16][i % Outer::kP * 32u + quarter * 8u]);
+      v[i] = *reinterpret_cast<const v8bf*>(&parts[i / Outer::kV][i16][i % Outer::kV * 32u + quarter * 8u]);
     }
   }
+  __syncthreads();
   o.columns(p, lds + wave * kMine, v, c, n1);
 }
 
 // Column slabs of a row tile.  Every slab makes the tile's inner values again,
-// so there are only as many as it takes to give the 256 CUs a workgroup each, and
-// half as many where the ranks make that work large.  us with 1 slab, with as
-// many as make 128, 256 and 512 workgroups (n, k, rank, tokens in adapters):
-//   2,048 x 2,048, 16, 64 in 24     8.4   6.9   6.2   6.2
-//   1,999 x 2,051, 24, 777 in 9    15.5  12.6  10.4  10.3
-//   2,048 x 2,048, 64, 4,001 in 9  18.6  18.1  18.0  23.3
-//   8,192 x 2,048, 64, 500 in 8    36.4  16.8  15.2  21.0
-//   4,096 x 4,096, 128, 1,000 in 8 48.4  38.1  57.5  75.7
+// so there are only as many as give each of the 256 CUs a workgroup, and no
+// more: one workgroup too many takes the time of two.  Each list of rows ends in
+// half a tile, about.  us with 1 slab, with as many as make up to 128, 256 and
+// 512 workgroups (n, k, rank, tokens in adapters):
+//   2,048 x 2,048, 16, 64 in 24      8.7   7.0   6.0   6.0
+//   1,999 x 2,051, 24, 777 in 9     15.4  12.7  10.2  10.1
+//   8,192 x 2,048, 16, 300 in 8     24.3  10.4   8.2   8.4
+//   4,096 x 4,096, 32, 1,000 in 8   18.8  18.9  12.9  16.1
+//   8,192 x 2,048, 64, 500 in 8     34.9  18.6  13.6  17.4
+//   4,096 x 4,096, 64, 1,000 in 8   25.0  25.2  17.5  23.4
+//   4,096 x 4,096, 128, 1,000 in 8  37.6  38.0  27.2  45.2
+//   8,192 x 8,192, 128, 300 in 8    68.0  40.3  35.7  61.2
 // (Inner and outer product in launches of their own, the inner values in memory
-// between them, took 4 to 10 us more than the best of these, except for 300 rows
-// of 8,192 at rank 128: 29 instead of 39.)
-uint32_t low_rank_slabs(uint64_t tiles, uint64_t n, uint64_t rank) {
-  const uint64_t most = cdiv(n, kLowRankSlab), want = tiles ? cdiv(rank > 64u ? 128u : 256u, tiles) : 1u;
+// between them, took 4 to 10 us more than the best of these, but for the last:
+// 29.)
+uint32_t low_rank_slabs(uint64_t tokens, uint64_t lists, uint64_t n) {
+  const uint64_t tiles = tokens / kLowRankRows + ((lists < tokens ? lists : tokens) + 1u) / 2u;
+  const uint64_t most = cdiv(n, kLowRankSlab), fit = tiles ? 256u / tiles : 1u, want = fit ? fit : 1u;
   const uint64_t slab = cdiv(cdiv(n, want < most ? want : most), kLowRankSlab) * kLowRankSlab;
   return uint32_t(cdiv(n, slab));
 }
@@ -552,7 +569,7 @@ ciera_status low_rank_add(const void* d_x, uint64_t ldx, const void* d_a, const 
   // every list of rows may end in a part of a tile
   const uint64_t lists = adapters + 2ull;
   const uint64_t tiles = tokens / kLowRankRows + (lists < tokens ? lists : tokens);
-  p.slabs = low_rank_slabs(tiles, n, rank);
+  p.slabs = low_rank_slabs(tokens, lists, n);
   p.slab = uint32_t(cdiv(cdiv(n, p.slabs), kLowRankSlab) * kLowRankSlab);
   const uint64_t grid = tiles ? tiles * p.slabs : 1u;
   if (grid > 0xFFFFFFFFull / kLowRankThreads) return CIERA_ERR_ARG;
