@@ -120,6 +120,30 @@ def test_values_at_the_edges():
         lu.within(y[i], want[i], 33 * U * want[i].abs(), 2.0 ** -8)
 
 
+@pytest.mark.parametrize("cols", [1, 3, 64, 300, 2049, 20001])
+@pytest.mark.parametrize("eps", [1e-6, 0.37, 1e-40])
+def test_root_of_exact_sums(cols, eps):
+    """Whole numbers whose squares' sum is exact (below 2^24): s has the two roundings of mean + eps, halved by the root,
+    and its own, so 2 u and what the correction leaves, below 2^-40."""
+    say(f"root of exact sums {cols} {eps}")
+    c = lib()
+    gen = torch.Generator().manual_seed(cols)
+    x = torch.randint(-15, 16, (200, cols), generator=gen).to(bf16)
+    x[0] = 0
+    y, s = torch.empty(200, cols, dtype=bf16, device="cuda"), torch.empty(200, device="cuda")
+    c.rms_norm(x.cuda(), torch.ones(cols, dtype=bf16).cuda(), y=y, rstd=s, eps=eps)
+    want = 1 / (x.double().square().sum(1) / cols + float(torch.tensor(eps))).sqrt()
+    lu.within(s, want, (2 * U + 2.0 ** -40) * want)
+
+
+def test_mean_and_eps_past_the_range():
+    c = lib()
+    x = torch.full((2, 1), 1.8e19, dtype=bf16, device="cuda")
+    y, s = torch.empty_like(x), torch.empty(2, device="cuda")
+    c.rms_norm(x, torch.ones(1, dtype=bf16, device="cuda"), y=y, rstd=s, eps=2e38)
+    assert (s == 0).all() and (y == 0).all()
+
+
 def backward64(dy, h, w, s, dh):
     hd, s = h.double(), s.double()[:, None]
     g, u = dy.double() * w.double(), hd * s
