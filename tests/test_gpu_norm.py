@@ -136,6 +136,24 @@ def test_root_of_exact_sums(cols, eps):
     lu.within(s, want, (2 * U + 2.0 ** -40) * want)
 
 
+@pytest.mark.parametrize("cols", [5, 300, 2048])
+def test_infinite_weights(cols):
+    """Infinities and NaN of the weight stay in their columns, with the sign that h has there."""
+    c = lib()
+    gen = torch.Generator().manual_seed(cols)
+    x, w = lu.mx.activations(gen, 20, cols), torch.randn(cols, generator=gen).to(bf16)
+    x[:, 1:3] = torch.where(x[:, 1:3] == 0, torch.ones((), dtype=bf16), x[:, 1:3])
+    y = torch.empty(20, cols, dtype=bf16, device="cuda")
+    w[1], w[2], w[4] = float("inf"), float("-inf"), float("nan")
+    c.rms_norm(x.cuda(), w.cuda(), y=y)
+    _, _, want = lu.norm(x, None, w, 1e-6)
+    assert torch.equal(y[:, 1].double().cpu(), want[:, 1]) and torch.equal(y[:, 2].double().cpu(), want[:, 2])
+    assert y[:, 4].isnan().all()
+    _, _, want = lu.norm(x, None, torch.where(w.isfinite(), w, torch.zeros((), dtype=bf16)), 1e-6)
+    keep = w.isfinite()
+    lu.within(y.cpu()[:, keep], want[:, keep], 33 * U * want[:, keep].abs(), 2.0 ** -8)
+
+
 def test_mean_and_eps_past_the_range():
     c = lib()
     x = torch.full((2, 1), 1.8e19, dtype=bf16, device="cuda")
