@@ -4,7 +4,8 @@ does the same for a linear layer on microscaled matrices; ``RmsNorm``,
 ``ExpertRows`` and ``LowRankAdapters`` for what stands around its products.
 
 Allocation happens only in the constructors; ``encode``/``decode`` only pass
-pointers.
+pointers.  The constructors fill what needs a value on the current stream:
+calls on another one are ordered behind that by the caller.
 """
 from __future__ import annotations
 
@@ -17,6 +18,16 @@ from . import (CieraError, ciera_decode, ciera_encode, ciera_encode_e0, ciera_en
                rms_norm, rms_norm_backward, rms_norm_workspace_size, zip3_decode, zip3_encode, zip3_encode_e0,
                zip3_encode_spec, zip3_max_encoded_size, zip3_workspace_size)
 
+_WS_HEAD = 256  # bytes of a workspace before its status words; their number is in there
+
+
+def _workspace(size: int, device):
+    """A workspace without status words, which reads as CIERA_OK: ``error``
+    before any call would else take their number from what the memory held."""
+    ws = torch.empty(size, dtype=torch.uint8, device=device)
+    ws[:_WS_HEAD].zero_()
+    return ws
+
 
 class Zip3Codec:
     """3-bit exponent code only (no cross-iteration state)."""
@@ -25,7 +36,7 @@ class Zip3Codec:
         self.n = n
         self.capacity = zip3_max_encoded_size(n)
         self.out = torch.empty(self.capacity, dtype=torch.uint8, device=device)
-        self.ws = torch.empty(zip3_workspace_size(n), dtype=torch.uint8, device=device)
+        self.ws = _workspace(zip3_workspace_size(n), device)
         self.size = torch.zeros(1, dtype=torch.int64, device=device)
 
     def encode(self, x, e0_override: int = -1, stream=None):
@@ -63,8 +74,8 @@ class CieraCodec:
         if self.capacity == 0:
             raise ValueError(f"invalid block size {B}")
         self.out = torch.empty(self.capacity, dtype=torch.uint8, device=device)
-        self.ws = torch.empty(ciera_workspace_size(n, B), dtype=torch.uint8, device=device)
-        self.ws_dec = torch.empty(ciera_workspace_size(n, B), dtype=torch.uint8, device=device)
+        self.ws = _workspace(ciera_workspace_size(n, B), device)
+        self.ws_dec = _workspace(ciera_workspace_size(n, B), device)
         self.size = torch.zeros(1, dtype=torch.int64, device=device)
         self.send_cache = torch.zeros(max(n, 1), dtype=torch.uint8, device=device)
         self.recv_cache = torch.zeros(max(n, 1), dtype=torch.uint8, device=device)
@@ -121,7 +132,7 @@ class MxLinear:
             raise ValueError(f"no workspace for {tokens} x {n} x {k} in {groups} groups")
         self.w = torch.empty(mx4_encoded_size(groups * n, k), dtype=torch.uint8, device=device)
         self.xq = torch.empty(mx8_encoded_size(tokens, k), dtype=torch.uint8, device=device)
-        self.ws = torch.empty(size, dtype=torch.uint8, device=device)
+        self.ws = _workspace(size, device)
         self.kept = None  # rows of the checkpoint in xq, None while there is none
 
     def load(self, weights, stream=None):
@@ -257,7 +268,7 @@ class ExpertRows:
         self.offsets = torch.zeros(experts + 1, dtype=torch.int64, device=device)
         self._place = torch.empty(tokens, choices, dtype=torch.int32, device=device)
         self._order = torch.empty(tokens * choices, dtype=torch.int32, device=device)
-        self.ws = torch.empty(size, dtype=torch.uint8, device=device)
+        self.ws = _workspace(size, device)
         self.place, self.order = self._place[:0], self._order[:0]
 
     def tokens(self) -> int:
@@ -314,7 +325,7 @@ class LowRankAdapters:
         self.b = torch.zeros(adapters, n, rank, dtype=torch.bfloat16, device=device)
         self.scales = torch.ones(adapters, dtype=torch.float32, device=device)
         self.rows = ExpertRows(tokens, 1, adapters, device)
-        self.ws = torch.empty(size, dtype=torch.uint8, device=device)
+        self.ws = _workspace(size, device)
 
     def load(self, index: int, a, b, scale: float = 1.0):
         """Adapter ``index``: a (r, k) and b (n, r), r at most the rank."""
