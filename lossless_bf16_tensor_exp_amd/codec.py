@@ -324,7 +324,7 @@ class LowRankAdapters:
         self.a = torch.zeros(adapters, rank, k, dtype=torch.bfloat16, device=device)
         self.b = torch.zeros(adapters, n, rank, dtype=torch.bfloat16, device=device)
         self.scales = torch.ones(adapters, dtype=torch.float32, device=device)
-        self.rows = ExpertRows(tokens, 1, adapters, device)
+        self.rows = self.taken = ExpertRows(tokens, 1, adapters, device)  # taken: the plan of the last add
         self.ws = _workspace(size, device)
 
     def load(self, index: int, a, b, scale: float = 1.0):
@@ -347,10 +347,14 @@ class LowRankAdapters:
         """y = base + the adapters' part; base may be y, or None for zeros."""
         rows = (self if plan is None else plan).rows
         low_rank_add(x, self.a, self.b, rows.offsets, y, self.ws, base, rows.order, self.scales, stream)
+        self.taken = rows
 
     def error(self, stream=None) -> int:
-        """Status of the last ``plan``, and of the last ``add``; synchronises."""
-        return ciera_read_error(self.rows.ws, stream) or ciera_read_error(self.ws, stream)
+        """Status of the last ``plan`` (CIERA_ERR_ARG for a number of no
+        adapter), of the plan that the last ``add`` took, and of that ``add``;
+        synchronises."""
+        taken = 0 if self.taken is self.rows else self.taken.error(stream)
+        return self.rows.error(stream) or taken or ciera_read_error(self.ws, stream)
 
 
 # One-shot calls: allocate the stream and workspace with torch, run one
