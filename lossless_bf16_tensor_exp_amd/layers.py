@@ -32,9 +32,11 @@ _functions = {}
 
 
 def _bind():
-    """The C functions by name."""
+    """The C functions by name.  The table is seen when all of it is there:
+    another thread may make its first call meanwhile."""
+    global _functions
     if not _functions:
-        lib = load_library()
+        lib, table = load_library(), {}
         m = [_vp, _u64]  # a matrix and its row stride, or a buffer and its length
         sigs = {
             "rms_norm_workspace_size": [_u64] * 2,
@@ -51,7 +53,8 @@ def _bind():
         for name, args in sigs.items():
             f = getattr(lib, name)
             f.argtypes, f.restype = args, _u64 if name.endswith("_size") else _int
-            _functions[name] = f
+            table[name] = f
+        _functions = table
     return _functions
 
 
