@@ -314,7 +314,9 @@ class LowRankAdapters:
     projection that all requests share: y = base + scale B (A x) by the adapter
     of each of up to ``tokens`` rows.  ``plan`` sorts a step's rows once for all
     its projections (another adapters' plan of the same rows can be given to
-    ``add``); rows of adapter -1 are base.  For serving: there is no gradient."""
+    ``add``); rows of adapter -1 are base.  ``load``, ``plan`` and ``add`` belong
+    to one stream, or are ordered by the caller.  For serving: there is no
+    gradient."""
 
     def __init__(self, tokens: int, n: int, k: int, rank: int, adapters: int, device="cuda"):
         size = low_rank_workspace_size(tokens, n, k, rank, adapters)
@@ -327,17 +329,18 @@ class LowRankAdapters:
         self.rows = self.taken = ExpertRows(tokens, 1, adapters, device)  # taken: the plan of the last add
         self.ws = _workspace(size, device)
 
-    def load(self, index: int, a, b, scale: float = 1.0):
+    def load(self, index: int, a, b, scale: float = 1.0, stream=None):
         """Adapter ``index``: a (r, k) and b (n, r), r at most the rank."""
         r = a.shape[0]
         if r > self.rank or tuple(a.shape) != (r, self.k) or tuple(b.shape) != (self.n, r):
             raise ValueError(f"a is {tuple(a.shape)} and b {tuple(b.shape)}, the adapters' are of rank {self.rank} for "
                              f"{self.n} x {self.k}")
-        self.a[index].zero_()
-        self.b[index].zero_()
-        self.a[index, :r] = a
-        self.b[index, :, :r] = b
-        self.scales[index] = scale
+        with torch.cuda.stream(stream):
+            self.a[index].zero_()
+            self.b[index].zero_()
+            self.a[index, :r] = a
+            self.b[index, :, :r] = b
+            self.scales[index] = scale
 
     def plan(self, ids, stream=None):
         """ids (tokens,) int32 or int64: each row's adapter, -1 for none."""
