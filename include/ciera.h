@@ -639,7 +639,8 @@ ciera_status expert_combine_backward(const void* d_dout, uint64_t lddout, const 
  * there.  Offsets out of order, or past tokens: as for the mx products.  An
  * order that names a row twice or leaves one out leaves those rows undefined;
  * a row out of range is left out.  The inner values A_a x_t are FP32; an
- * infinity in d_b gives NaN. */
+ * infinity in d_b gives what the formula gives (an inner value of less than
+ * 2^-126 may count as zero there: NaN). */
 uint64_t low_rank_workspace_size(uint64_t tokens, uint64_t n, uint64_t k, uint64_t rank, uint32_t adapters);
 ciera_status low_rank_add(const void* d_x, uint64_t ldx, const void* d_a, const void* d_b, const float* d_scales,
                           const int64_t* d_offsets, const int32_t* d_order, const void* d_base, uint64_t ldb,

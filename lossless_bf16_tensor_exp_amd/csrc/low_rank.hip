@@ -124,7 +124,8 @@ __device__ __forceinline__ void low_rank_report(const LowRankArgs& p) {
 
 // v as three BF16 numbers whose sum it is: its leading 8 significant bits, the
 // next 8 and the last.  Cut, not rounded, so that none passes BF16's range;
-// an infinity or a NaN is the first alone.
+// an infinity or a NaN is the first alone.  The first is zero only for a v of
+// less than 2^-126.
 __device__ __forceinline__ void low_rank_split(float v, uint16_t (&part)[3]) {
   const uint32_t b = __float_as_uint(v);
   if ((b & 0x7F800000u) == 0x7F800000u) {
@@ -244,7 +245,7 @@ struct LowRankOuter {
   static constexpr uint32_t kFrag = 17u * kRow;            // bytes from one fragment to the next
   static constexpr uint32_t kLds = 4u * kFrag;
   const uint16_t* b;
-  uint64_t row[4];
+  uint32_t row[4];
   bool live[4];
   u32x4v w[kLoads];
   u32x4v base[4];  // BF16: the first half
@@ -268,13 +269,21 @@ struct LowRankOuter {
       w[i] = row_load8(b + uint64_t(min(c + i * kPer + lane / kChunks, p.n - 1u)) * p.rank,
                        piece * (kRow / 2u) + lane % kChunks * 8u, p.rank);
   }
+  // Where row r begins (a stride is less than 2^32).  With 17 to 64 ranks made at each use: kept from step to step, the
+  // four rows' places in base and in y take 16 registers, and onto an FP32 base at rank 64 some of them memory (16,384
+  // rows 98 us instead of 92; at rank 32 55 instead of 53; at rank 16 45 instead of 47, at 128 123 instead of 125).
+  __device__ __forceinline__ uint64_t offset(uint32_t r, uint64_t ld) const {
+    uint32_t of = row[r];
+    if constexpr (kF == 2u || kF == 4u) asm volatile("" : "+v"(of));
+    return uint64_t(of) * uint32_t(ld);
+  }
   // this lane's four columns of its four rows: whole where none passes the end
   __device__ __forceinline__ void load_base(const LowRankArgs& p, uint32_t c) {
     const uint32_t col = c + (threadIdx.x & 15u) * 4u;
     if (!p.base) return;
 #pragma unroll
     for (uint32_t r = 0; r < 4u; r++) {
-      const uint64_t from = row[r] * p.ldb + col;
+      const uint64_t from = offset(r, p.ldb) + col;
       if constexpr (kF32) {
         const float* f = static_cast<const float*>(p.base) + from;
         if (col + 4u <= p.n) {
@@ -311,7 +320,7 @@ struct LowRankOuter {
 #pragma unroll
       for (uint32_t f = 0; f < 4u; f++) v[f] = value(p, r, f) + sum[f][r];
       if (!live[r]) continue;
-      const uint64_t to = row[r] * p.ldy + col;
+      const uint64_t to = offset(r, p.ldy) + col;
       if (p.y_f32) {
         float* o = static_cast<float*>(p.y) + to;
         if (col + 4u <= p.n) {
@@ -330,6 +339,41 @@ struct LowRankOuter {
           for (uint32_t i = 0; i < 3u; i++)
             if (col + i < p.n) o[i] = mx_bf16(v[i]);
         }
+      }
+    }
+  }
+  // The sums of columns c .. c + 63 once more, where there is a NaN: an infinity of B times a part of v that is zero is
+  // one, also where v is not zero.  The parts behind v's first see zeros for what is not finite in B, which times the
+  // first part is what it is times v.  The other sums keep their bits: equal terms in equal order.  (Looking for a NaN:
+  // 16,384 rows at rank 128 124.3 us instead of 123.1, up to rank 64 nothing that shows.)
+  __device__ __forceinline__ void again(const LowRankArgs& p, const uint8_t* lds, const v8bf (&v)[kSteps], uint32_t c, v4f (&sum)[4]) const {
+    const uint32_t i16 = threadIdx.x & 15u, quarter = (threadIdx.x >> 4) & 3u;
+#pragma unroll
+    for (uint32_t f = 0; f < 4u; f++) {
+      sum[f] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (uint32_t step = 0; step < kV; step++) {
+        u32x4v w;
+        if constexpr (kP == 1u)  // the piece is still there
+          w = *reinterpret_cast<const u32x4v*>(lds + at(f, i16, kF == 1u ? quarter & 1u : step * 4u + quarter));
+        else
+          w = row_get8<false>(b + uint64_t(min(c + i16 * 4u + f, p.n - 1u)) * p.rank, (step * 4u + quarter) * 8u, p.rank);
+        const v8bf all = __builtin_bit_cast(v8bf, w);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          if ((w[i] & 0x7F80u) == 0x7F80u) w[i] &= 0xFFFF0000u;
+          if ((w[i] & 0x7F800000u) == 0x7F800000u) w[i] &= 0xFFFFu;
+        }
+        const v8bf fine = __builtin_bit_cast(v8bf, w);
+        if constexpr (kF == 1u) {
+          sum[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[1], fine, sum[f], 0, 0, 0);
+          sum[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[0], quarter < 2u ? all : fine, sum[f], 0, 0, 0);
+        } else {
+#pragma unroll
+          for (uint32_t part = 3u; part > 0u; part--)
+            sum[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[(part - 1u) * kV + step], part > 1u ? fine : all, sum[f], 0, 0, 0);
+        }
+        loads_first();
       }
     }
   }
@@ -372,6 +416,9 @@ struct LowRankOuter {
         }
         wave_lds();
       }
+      loads_first();
+      const v4f t = (sum[0] + sum[1]) + (sum[2] + sum[3]);  // NaN if one of them is (or by overflow, which costs time alone)
+      if (__any(__builtin_isnan((t[0] + t[1]) + (t[2] + t[3])))) again(p, lds, v, c, sum);
       store(p, c, sum);
       if (c + 64u < n1) load_base(p, c + 64u);
     }
