@@ -458,9 +458,11 @@ def bind(name: str, *args, stream=None):
 
 
 def ciera_read_error(ws, stream=None) -> int:
-    """Synchronise the stream and return the device-side status word."""
+    """Synchronise the stream, the current one of the workspace's device unless
+    one is given, and return the device-side status word."""
     _check_bytes(ws, "ws")
-    return load_library().ciera_read_error(_ptr(ws), _stream(stream))
+    with _torch().cuda.device(ws.device):
+        return load_library().ciera_read_error(_ptr(ws), _stream(stream))
 
 
 def ciera_time_kernels(pairs, stream=None) -> None:
