@@ -330,12 +330,13 @@ class LowRankAdapters:
         self.ws = _workspace(size, device)
 
     def load(self, index: int, a, b, scale: float = 1.0, stream=None):
-        """Adapter ``index``: a (r, k) and b (n, r), r at most the rank."""
+        """Adapter ``index``: a (r, k) and b (n, r), r at most the rank; their
+        values alone, autograd records nothing."""
         r = a.shape[0]
         if r > self.rank or tuple(a.shape) != (r, self.k) or tuple(b.shape) != (self.n, r):
             raise ValueError(f"a is {tuple(a.shape)} and b {tuple(b.shape)}, the adapters' are of rank {self.rank} for "
                              f"{self.n} x {self.k}")
-        with torch.cuda.stream(stream):
+        with torch.no_grad(), torch.cuda.stream(stream):
             self.a[index].zero_()
             self.b[index].zero_()
             self.a[index, :r] = a

@@ -79,3 +79,18 @@ def test_an_adapter_replaced_between_two_steps():
     for y, (a, b, scales) in ((y1, was), (y2, now)):
         want, size = lu.low_rank(x, a, b, scales, offsets, order, torch.zeros(tokens, n))
         lu.within(y, want, (k + 3 * rank + 4) * U * size + U * want.abs(), U)
+
+
+def test_trained_parameters_leave_no_graph():
+    """Adapters as a training loop holds them: the buffers take their values and keep nothing of them."""
+    from lossless_bf16_tensor_exp_amd.codec import LowRankAdapters
+    low = LowRankAdapters(4, 16, 8, 4, 2, device="cpu")
+    a = torch.nn.Parameter(torch.full((3, 8), 2.0, dtype=bf16))
+    b = torch.nn.Parameter(torch.full((16, 3), 3.0, dtype=bf16))
+    scale = torch.nn.Parameter(torch.tensor(0.25))
+    for _ in range(2):
+        low.load(1, a * 2, b, scale)
+        for t in (low.a, low.b, low.scales):
+            assert not t.requires_grad and t.grad_fn is None
+    assert (low.a[1, :3] == 4).all() and (low.b[1, :, :3] == 3).all() and low.scales[1] == 0.25
+    assert torch.is_grad_enabled()
