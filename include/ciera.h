@@ -255,7 +255,9 @@ ciera_status ciera_decode_batch(uint32_t k, const void* const* d_in, const uint6
 
 /* Synchronise `stream` and return the device-side status of the last call
  * that used d_ws: CIERA_OK, CIERA_ERR_FORMAT (decode saw a malformed
- * stream), CIERA_ERR_INTERNAL, or CIERA_ERR_HIP if the copy fails. */
+ * stream), CIERA_ERR_INTERNAL, or CIERA_ERR_HIP if the copy fails.  A
+ * workspace that no call has used yet reads as CIERA_OK if its first 256 bytes
+ * are zero; with other bytes there it must not be read. */
 ciera_status ciera_read_error(const void* d_ws, hipStream_t stream);
 
 /* zip3_encode_e0: zip3 encode with the window base read from device memory

@@ -104,8 +104,9 @@ __global__ __launch_bounds__(1024) void k_sort_count(SortArgs p) {
   if (threadIdx.x == 0u) p.counts[uint64_t(p.blocks) * bins + blockIdx.x] = any;
 }
 
-// Bound by launches and by dependent steps: 32,768 entries of 64 experts 4.0 us
-// for the counts and 5.2 here, of which 2.5 are each one's launch.
+// Bound by launches and by dependent steps: 32,768 entries of 64 experts 4.7 us
+// for the counts and 5.4 here (medians of a profiler's trace), of which 2.5 are
+// each one's launch.
 // Each wave takes a stretch of the entries and counts it; the counts become
 // the places where the wave's entries of each bin begin; then the wave goes
 // through its stretch again, 64 entries a step.  Lanes of one bin find each
@@ -370,7 +371,9 @@ __global__ __launch_bounds__(256) void k_combine(RowArgs p) {
 
 // dout is read again for each kRowsAtOnce of the choices (from L2).  Bound by
 // memory: 4,096 x 8 rows of 2,048, 286 MB: 55 us, 5.2 TB/s; rows and their
-// gradients go past the last-level cache (62 us through it).
+// gradients go past the last-level cache (62 us through it).  With fewer choices
+// than kRowsAtOnce fewer loads are in flight behind each barrier: 16,384 x 2 rows
+// 62 us on 54 for the bytes, 32,768 x 1 96 on 64.
 template <bool kWave, bool kF32>
 __global__ __launch_bounds__(256) void k_combine_back(RowArgs p) {
   __shared__ float part[2][4][kRowsAtOnce];

@@ -14,13 +14,16 @@
 // parts that hold its 24 significant bits, so that nothing is rounded between
 // the two products.
 //
-// What bounds it: for few rows the launch and one pass through dependent loads
-// (64 rows of 24 adapters, rank 16, k = n = 2,048: 5.9 us, of which 2.5 launch);
-// for many, memory in two phases, x and then base and y, that overlap only
-// between workgroups (16,384 rows at rank 16, 201 MB: 45 us, 4.5 TB/s), and from
-// rank 64 on the way of A and B through LDS, once for each row tile (4,001 rows
-// at rank 64, 53 MB: 16.2 us; 16,384: 72).  Base or v's loads further ahead
-// gained nothing.
+// What bounds it (us by the launches' own events): for few rows the launch and
+// one pass through dependent loads (64 rows of 24 adapters, rank 16, k = n =
+// 2,048: 5.8 us, of which 2.5 launch); for few rows of a large rank and a long
+// contraction A x, which every slab of columns makes again (16 rows, k = n =
+// 8,192, rank 64: 19 on 2.8 for the bytes); for many rows memory in two phases,
+// x and then base and y, that overlap only between workgroups (16,384 rows at
+// rank 16, 201 MB: 45 us, 4.5 TB/s), and from rank 64 on the way of A and B from
+// L2 through LDS, 512 KB for each tile of 16 rows (4,001 rows at rank 64, 53 MB:
+// 16.4 us; 16,384: 73; at rank 128 124).  Base or v's loads further ahead gained
+// nothing.
 #include "ciera.h"
 
 namespace {

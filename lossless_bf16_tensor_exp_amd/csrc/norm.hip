@@ -17,7 +17,18 @@
 namespace {
 
 constexpr uint32_t kNormMaxCols = 32768u;  // 1,024 threads of four units of 8 values
-constexpr uint32_t kNormParts = 512u;      // workgroups of the backward pass, each with a sum of dw of its own
+
+// Workgroups of the backward pass, each with a sum of dw of its own.  us, with
+// the join of the sums, with 256, 512, 768 and 1,024 of them (with dh, dw FP32):
+//   262,144 x 64      48   34   31   33
+//   65,536 x 512      62   50   52   52
+//   32,768 x 1,000    67   50   52   56
+//   16,384 x 2,048    67   52   59   53
+//   8,192 x 4,096     65   53   61   56
+//   4,096 x 8,192     59   58   65   67
+//   1,677 x 20,000    85   94  108  125
+//   1,024 x 32,768    86  113  139  160
+constexpr uint32_t kNormParts = 512u;
 
 template <uint32_t k>
 using Num = std::integral_constant<uint32_t, k>;
@@ -237,10 +248,13 @@ struct NormBackArgs {
 // A workgroup takes every parts-th stretch of kB / kT * kN rows, a thread's
 // loads of kN rows at once (with one barrier for their sums), and keeps its sums
 // of dw in registers to the end.  Bound by memory: 16,384 x 2,048 with dh, 268
-// MB: 48 us, 5.6 TB/s (53 through the last-level cache), and 4 for the sums of
-// dw, 512 workgroups' (768: 59 and 4.5; 256: 66 and 4).  Registers leave two
-// waves a SIMD, whose 48 KB in flight a CU are enough.  Two rows of 4,096 with 256
-// threads: 8,000 of them 53 us; four with 512 threads 64.
+// MB: 48 us, 5.6 TB/s (53 through the last-level cache), and 4 for the join of
+// the sums.  Registers leave two waves a SIMD (up to 1,024 columns three), two
+// workgroups a CU, each with 48 KB in flight.  Two rows of 4,096 with 256
+// threads: 8,000 of them 53 us; four with 512 threads 64.  Past 8,192 columns a
+// row is read twice by one workgroup of 16 waves a CU: 1,024 x 32,768 100 us
+// (and 12) on 43 for the bytes; of odd length 129, with some registers in memory
+// (18 of a thread's).
 template <uint32_t kT, uint32_t kU, uint32_t kN, bool kWhole>
 __global__ __launch_bounds__(kT < 256u ? 256u : kT) void k_rms_norm_back(NormBackArgs p) {
   constexpr uint32_t kB = kT < 256u ? 256u : kT, kSubs = kB / kT;
